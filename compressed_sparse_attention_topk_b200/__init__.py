@@ -9,7 +9,9 @@ a CUDA device, the call raises.
 Functions mirror the C entry points: ``pack_fp4``, ``unpack_fp4``,
 ``index_topk``, ``sparse_attn_decode``, ``sparse_attn_prefill``,
 ``layer_group_run``, plus ``validate_modes``, ``group_cache_bytes`` and
-``get_device_status``.
+``get_device_status``; and, for the 8-bit paged key/value cache (``KV8Cache``),
+``block_tables``, ``kv8_append``, ``kv8_unpack``, ``kv8_select`` and
+``kv8_attn``.
 """
 from __future__ import annotations
 
@@ -35,7 +37,9 @@ EXPORTED = (
     "csa2_index_pool", "csa2_pool_topk_workspace_size", "csa2_pool_topk", "csa2_append_entry",
     "csa2_pack_index_keys_fp4", "csa2_index_topk_fp4k_workspace_size", "csa2_index_topk_fp4k",
     "csa2_wait_timeout_selftest", "csa2_set_decode_kernel", "csa2_get_decode_kernel",
-    "csa2_stage_copies",
+    "csa2_stage_copies", "csa2_block_tables", "csa2_kv8_append", "csa2_kv8_unpack",
+    "csa2_kv8_select_workspace_size", "csa2_kv8_select", "csa2_kv8_attn_workspace_size",
+    "csa2_kv8_attn",
 )
 DECODE_SCAN_CLUSTER, DECODE_FUSED = 0, 1
 
@@ -63,6 +67,13 @@ class Copy2D(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("row_bytes", ctypes.c_int64), ("src_stride", ctypes.c_int64),
                 ("dst_stride", ctypes.c_int64)]
+
+
+class KV8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_sum", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("Hk", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("D", ctypes.c_int32)]
 
 
 MAX_STAGE_COPIES = 16
@@ -116,6 +127,15 @@ def lib() -> ctypes.CDLL:
         "csa2_pool_topk_workspace_size": ([i32, i32, i32], sz),
         "csa2_pool_topk": ([P, P, P, i32, i32, i32, i64, P, i32, i32, P, P, sz, P], i32),
         "csa2_stage_copies": ([P, i32, P], i32),
+        "csa2_block_tables": ([P, P, i32, i32, P, i32, P, i32, P, P, P, P, i64, P, P], i32),
+        "csa2_kv8_append": ([P, P, i64, P, i64, P, i64, P], i32),
+        "csa2_kv8_unpack": ([P, P, i64, P, P, P], i32),
+        "csa2_kv8_select_workspace_size": ([i64, i32, i32], sz),
+        "csa2_kv8_select": ([P, i64, P, P, i32, P, P, i32, i64, i32, i32, i32, i32, P, P, sz, P],
+                            i32),
+        "csa2_kv8_attn_workspace_size": ([i64, i32, i32, i32, i32, i32], sz),
+        "csa2_kv8_attn": ([P, i64, P, P, i32, P, P, i32, i64, i32, P, i32, f32, P, P, P, sz, P],
+                          i32),
         "csa2_get_device_status": ([P, P], i32),
         "csa2_wait_timeout_selftest": ([i64, P], i32),
         "csa2_set_decode_kernel": ([i32], i32),
@@ -455,6 +475,223 @@ def sparse_attn_prefill(q, codes, scales, idx, win_k, win_v, sm_scale: Optional[
                                           _ptr(win_k), _ptr(win_v), B, T, H, D, N, topk, W,
                                           sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
                                           _stream()), "csa2_sparse_attn_prefill")
+    return out, lse
+
+
+# --- 8-bit paged key/value cache ------------------------------------------------
+
+def block_tables(lens, add, table, free_pages, block: int, cap: int, out=None):
+    """Block tables and slot maps of a step: request b holds lens[b] tokens and
+    adds add[b] (int32 [B]); the pages it needs are taken, request by request,
+    from the front of free_pages (int32) and written into its row of table
+    (int32 [B, width], updated).  Returns (lens + add int32 [B], cu int32
+    [B+1], slots int64 [cap], pos int32 [cap], used int32 [1]): token offsets,
+    each token's slot (page * block + row) and position (-1 past the last
+    token), pages taken.  ``out``: those five tensors, to write into."""
+    torch = _torch()
+    lens = _dev(lens, "lens", torch.int32)
+    add = _dev(add, "add", torch.int32)
+    table = _dev(table, "table", torch.int32)
+    free_pages = _dev(free_pages, "free_pages", torch.int32)
+    B, width = table.shape
+    if lens.shape != (B,) or add.shape != (B,) or free_pages.dim() != 1:
+        raise ValueError("lens and add are [B], table [B, width], free_pages [n]")
+    if out is None:
+        new = lens.new_empty
+        out = (new(B), new(B + 1), new(cap, dtype=torch.int64), new(cap), new(1))
+    else:
+        for t, name, n, dt in zip(out, ("lens", "cu", "slots", "pos", "used"),
+                                  (B, B + 1, cap, cap, 1),
+                                  (torch.int32, torch.int32, torch.int64, torch.int32,
+                                   torch.int32)):
+            if _dev(t, "out." + name, dt).numel() != n:
+                raise ValueError(f"out.{name} must have {n} elements")
+    lens_out, cu, slots, pos, used = out
+    _here(lens, add, table, free_pages, *out)
+    _check(lib().csa2_block_tables(_ptr(lens), _ptr(add), B, block, _ptr(table), width,
+                                   _ptr(free_pages), free_pages.shape[0], _ptr(lens_out),
+                                   _ptr(cu), _ptr(slots), _ptr(pos), cap, _ptr(used), _stream()),
+           "csa2_block_tables")
+    return out
+
+
+class KV8Cache:
+    """The tensors of an 8-bit paged cache, checked and marshalled once: int8
+    k, v [pages, Hk, block, D], fp32 k_scale, v_scale [pages, Hk], int16 k_sum
+    [pages, Hk, D] (contiguous CUDA tensors, kept alive by this handle)."""
+
+    def __init__(self, k, v, k_scale, v_scale, k_sum):
+        torch = _torch()
+        self.k, self.v = _dev(k, "k", torch.int8), _dev(v, "v", torch.int8)
+        self.k_scale = _dev(k_scale, "k_scale", torch.float32)
+        self.v_scale = _dev(v_scale, "v_scale", torch.float32)
+        self.k_sum = _dev(k_sum, "k_sum", torch.int16)
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, Hk, block, D]")
+        self.pages, self.Hk, self.block, self.D = k.shape
+        P, Hk, D = self.pages, self.Hk, self.D
+        if (v.shape != k.shape or k_scale.shape != (P, Hk) or v_scale.shape != (P, Hk)
+                or k_sum.shape != (P, Hk, D)):
+            raise ValueError("v must be like k, k_scale and v_scale [pages, Hk], k_sum "
+                             "[pages, Hk, D]")
+        if any(x.get_device() != k.get_device() for x in (v, k_scale, v_scale, k_sum)):
+            raise ValueError("the tensors of a cache must be on one device")
+        self._c = KV8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_sum), P, Hk,
+                      self.block, D)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, Hk: int, block: int, D: int, device="cuda") -> "KV8Cache":
+        """A new cache, all zeros."""
+        torch = _torch()
+
+        def zeros(shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        return cls(zeros((pages, Hk, block, D), torch.int8), zeros((pages, Hk, block, D),
+                                                                   torch.int8),
+                   zeros((pages, Hk), torch.float32), zeros((pages, Hk), torch.float32),
+                   zeros((pages, Hk, D), torch.int16))
+
+
+def _here(*tensors):
+    """Every tensor on the current CUDA device: the calls launch on its
+    current stream."""
+    dev = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{dev}")
+
+
+def _scratch(nbytes, ws, device):
+    """The caller's workspace, or a new one of this call: from the caching
+    allocator, so calls on other streams and captured graphs never share it."""
+    if ws is not None:
+        return _dev(ws, "ws", _torch().uint8)
+    return _torch().empty(max(nbytes, 256), dtype=_torch().uint8, device=device)
+
+
+def _tokens(t, name, D, heads=None):
+    """A bf16 [n, heads, D] CUDA tensor whose tokens may be strided, the heads
+    of a token dense; returns its token stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {D}]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (t.shape[1] > 1 and s1 != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return s0 if t.shape[0] > 1 else max(s0, t.shape[1] * D)
+
+
+def _step(cache, table, cu, lens):
+    torch = _torch()
+    _dev(table, "table", torch.int32)
+    _dev(cu, "cu", torch.int32)
+    _dev(lens, "lens", torch.int32)
+    B, width = table.shape
+    if cu.shape != (B + 1,) or lens.shape != (B,):
+        raise ValueError("table is [B, width], cu [B+1], lens [B]")
+    return B, width
+
+
+def kv8_append(cache: KV8Cache, k_new, v_new, slots):
+    """Write tokens' keys and values (bf16 [n, Hk, D], tokens may be strided)
+    at their slots (int64 [n], page * block + row; negative: nothing), in
+    place.  The tokens of a page are consecutive, at ascending rows."""
+    ks = _tokens(k_new, "k_new", cache.D, cache.Hk)
+    vs = _tokens(v_new, "v_new", cache.D, cache.Hk)
+    _dev(slots, "slots", _torch().int64)
+    n = slots.shape[0]
+    if k_new.shape[0] != n or v_new.shape[0] != n:
+        raise ValueError("k_new, v_new and slots must have one row per token")
+    _here(cache.k, k_new, v_new, slots)
+    _check(lib().csa2_kv8_append(cache._ref, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(slots), n,
+                                 _stream()), "csa2_kv8_append")
+
+
+def kv8_unpack(cache: KV8Cache, slots, k_out=None, v_out=None):
+    """The rows at slots (int64 [n]) as fp32 [n, Hk, D] keys and values (zeros
+    for a negative slot)."""
+    torch = _torch()
+    _dev(slots, "slots", torch.int64)
+    shape = (slots.shape[0], cache.Hk, cache.D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.float32, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.float32, device=slots.device)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if _dev(t, name, torch.float32).shape != shape:
+            raise ValueError(f"{name} must be [n, Hk, D]")
+    _here(cache.k, slots, k_out, v_out)
+    _check(lib().csa2_kv8_unpack(cache._ref, _ptr(slots), shape[0], _ptr(k_out), _ptr(v_out),
+                                 _stream()), "csa2_kv8_unpack")
+    return k_out, v_out
+
+
+def kv8_select_workspace_size(n, Hk, width) -> int:
+    return int(lib().csa2_kv8_select_workspace_size(n, Hk, width))
+
+
+def kv8_select(q, cache: KV8Cache, table, cu, lens, n_sel: int, n_first: int = 1,
+               n_last: int = 1, out=None, ws=None):
+    """The n_sel blocks that each token (q bf16 [n, H, D]) and kv head attends
+    to: its first n_first, its last n_last and the best-scored others, int32
+    [n, Hk, n_sel] ascending, then -1.  table int32 [B, width], cu int32
+    [B+1] token offsets, lens int32 [B] tokens in the cache."""
+    torch = _torch()
+    stride = _tokens(q, "q", cache.D)
+    B, width = _step(cache, table, cu, lens)
+    n, H = q.shape[:2]
+    if out is None:
+        out = torch.empty((n, cache.Hk, n_sel), dtype=torch.int32, device=q.device)
+    elif _dev(out, "out", torch.int32).shape != (n, cache.Hk, n_sel):
+        raise ValueError("out must be [n, Hk, n_sel]")
+    ws = _scratch(kv8_select_workspace_size(n, cache.Hk, width), ws, q.device)
+    _here(q, cache.k, table, cu, lens, out, ws)
+    _check(lib().csa2_kv8_select(_ptr(q), stride, cache._ref, _ptr(table), width, _ptr(cu),
+                                 _ptr(lens), B, n, H, n_sel, n_first, n_last, _ptr(out), _ptr(ws),
+                                 ws.numel(), _stream()), "csa2_kv8_select")
+    return out
+
+
+def kv8_attn_workspace_size(n, B, H, Hk, D, n_sel=0) -> int:
+    return int(lib().csa2_kv8_attn_workspace_size(n, B, H, Hk, D, n_sel))
+
+
+def kv8_attn(q, cache: KV8Cache, table, cu, lens, sel=None, sm_scale: Optional[float] = None,
+             out=None, lse=None, ws=None):
+    """Causal attention of a step's tokens over the cache (their own keys and
+    values already appended): q bf16 [n, H, D], table int32 [B, width], cu
+    int32 [B+1], lens int32 [B]; sel int32 [n, Hk, n_sel]: only the listed
+    blocks -> (out bf16 [n, H, D], lse fp32 [n, H])."""
+    torch = _torch()
+    stride = _tokens(q, "q", cache.D)
+    B, width = _step(cache, table, cu, lens)
+    n, H = q.shape[:2]
+    n_sel = 0
+    if sel is not None:
+        if _dev(sel, "sel", torch.int32).dim() != 3 or sel.shape[:2] != (n, cache.Hk):
+            raise ValueError("sel must be [n, Hk, n_sel]")
+        n_sel = sel.shape[2]
+    if out is None:
+        out = torch.empty((n, H, cache.D), dtype=torch.bfloat16, device=q.device)
+    elif _dev(out, "out", torch.bfloat16).shape != (n, H, cache.D):
+        raise ValueError("out must be [n, H, D]")
+    if lse is None:
+        lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
+    elif _dev(lse, "lse", torch.float32).shape != (n, H):
+        raise ValueError("lse must be [n, H]")
+    ws = _scratch(kv8_attn_workspace_size(n, B, H, cache.Hk, cache.D, n_sel), ws, q.device)
+    _here(q, cache.k, table, cu, lens, sel, out, lse, ws)
+    sm_scale = 1.0 / math.sqrt(cache.D) if sm_scale is None else sm_scale
+    _check(lib().csa2_kv8_attn(_ptr(q), stride, cache._ref, _ptr(table), width, _ptr(cu),
+                               _ptr(lens), B, n, H, _ptr(sel), n_sel, sm_scale, _ptr(out),
+                               _ptr(lse), _ptr(ws), ws.numel(), _stream()), "csa2_kv8_attn")
     return out, lse
 
 

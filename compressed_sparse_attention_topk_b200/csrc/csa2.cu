@@ -1,6 +1,7 @@
 // C ABI of the CSA2 hot path (see include/csa2.h for the contract of every
-// entry point).  One translation unit: every kernel of the library is
-// included here so that they share the device status word.
+// entry point), but for the paged key/value cache (kv8.cu).  One translation
+// unit: every kernel of the path is included here so that they share the
+// device status word.
 #include "csa2.h"
 
 #include <algorithm>
@@ -15,91 +16,20 @@
 #include "common.cuh"
 #include "stage.cuh"
 #include "decode_fused.cuh"
+#include "host.cuh"
 #include "index_scan.cuh"
 #include "pack.cuh"
 #include "pool.cuh"
 #include "prefill_gemm.cuh"
 #include "row_cluster.cuh"
 
+namespace csa2 {
+csa2_status kv8_take_status(uint32_t *v);  // kv8.cu
+}
+
 using namespace csa2;
 
 namespace {
-
-inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
-
-int device_sms() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  static std::atomic<int> cache[256];  // per device: 0 unknown
-  if (dev >= 0 && dev < 256) {
-    const int c = cache[dev].load(std::memory_order_relaxed);
-    if (c) return c;
-  }
-  int v = 148;
-  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) v = 148;
-  if (dev >= 0 && dev < 256) cache[dev].store(v, std::memory_order_relaxed);
-  return v;
-}
-
-csa2_status after_launch() { return cudaGetLastError() == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
-
-// ---------------------------------------------------------------------------
-// Kernel timing trace: event pairs around launches while enabled.
-// ---------------------------------------------------------------------------
-struct TraceRecord {
-  const char *name;
-  cudaEvent_t start, stop;
-};
-constexpr size_t kTraceMax = size_t(1) << 16;
-bool g_trace_on = false;
-TraceRecord *g_trace = nullptr;
-size_t g_trace_n = 0;
-
-void trace_clear() {
-  for (size_t i = 0; i < g_trace_n; ++i) {
-    cudaEventDestroy(g_trace[i].start);
-    cudaEventDestroy(g_trace[i].stop);
-  }
-  g_trace_n = 0;
-}
-
-// Records an event on `st`; while `st` is being captured into a CUDA graph
-// the record becomes an event-record node of the graph (timed on every
-// replay) instead of a capture-internal dependency.
-inline void trace_record(cudaEvent_t ev, cudaStream_t st) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive)
-    cudaEventRecordWithFlags(ev, st, cudaEventRecordExternal);
-  else
-    cudaEventRecord(ev, st);
-}
-
-// Brackets one launch: records `start` on construction and `stop` on
-// destruction when the trace is on and has room.
-struct TraceScope {
-  TraceRecord *rec = nullptr;
-  cudaStream_t st;
-  TraceScope(const char *name, cudaStream_t s) : st(s) {
-    if (!g_trace_on || g_trace_n >= kTraceMax) return;
-    if (!g_trace) g_trace = new TraceRecord[kTraceMax];
-    TraceRecord &r = g_trace[g_trace_n];
-    if (cudaEventCreate(&r.start) != cudaSuccess) return;
-    if (cudaEventCreate(&r.stop) != cudaSuccess) {
-      cudaEventDestroy(r.start);
-      return;
-    }
-    r.name = name;
-    rec = &r;
-    ++g_trace_n;
-    trace_record(r.start, st);
-  }
-  ~TraceScope() {
-    if (rec) trace_record(rec->stop, st);
-  }
-};
 
 // ---------------------------------------------------------------------------
 // Index + top-k: shapes, workspace, launches.
@@ -168,21 +98,6 @@ HandoffWs handoff_layout(void *base, int64_t R, int32_t topk, int32_t H, int32_t
   w.lists = reinterpret_cast<int32_t *>(p + o_lists);
   w.part = reinterpret_cast<float *>(p + o_part);
   return w;
-}
-
-// Per-device one-time kernel attribute setup (dynamic shared memory above
-// 48 KiB, non-portable cluster size).  Must run before any stream capture;
-// the entry points call it on their first use on a device.
-template <typename K>
-csa2_status set_smem_attr(K kernel, size_t bytes, bool big_cluster) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-      cudaSuccess)
-    return CSA2_ERR_CUDA;
-  if (big_cluster &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-          cudaSuccess)
-    return CSA2_ERR_CUDA;
-  return CSA2_OK;
 }
 
 // Index-key format of a scan: int8 keys, or FP4 keys (k_exps != nullptr).
@@ -621,46 +536,6 @@ int64_t pf_rows_per_pass(int32_t T, int64_t N, int32_t d_I) {
 
 size_t pf_ws_bytes(int32_t T, int64_t N, int32_t d_I) {
   return pf_ws_layout(nullptr, pf_rows_per_pass(T, N, d_I), N, d_I).bytes;
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// dependency on the driver library).
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = [] {  // looked up once (thread-safe initialisation)
-    EncodeTiledFn f = nullptr;
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      f = reinterpret_cast<EncodeTiledFn>(ptr);
-    cudaGetLastError();
-    return f;
-  }();
-  return fn;
-}
-
-// 3-D byte tensor map: dims {d0, d1, d2}, byte strides of dims 1 and 2, box
-// {d0, b1, b2}, swizzled over d0 bytes (d0 in {32, 64, 128}).
-bool make_map_u8(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
-                 uint64_t s1, uint64_t s2, uint32_t b1, uint32_t b2) {
-  EncodeTiledFn f = encode_tiled();
-  if (!f || d1 == 0 || d2 == 0) return false;
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {s1, s2};
-  const cuuint32_t box[3] = {(cuuint32_t)d0, b1, b2};
-  const cuuint32_t es[3] = {1, 1, 1};
-  const CUtensorMapSwizzle sw = d0 == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : d0 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                           : CU_TENSOR_MAP_SWIZZLE_32B;
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Shapes the tensor-core prefill path serves (host arithmetic only: the
@@ -2231,6 +2106,10 @@ csa2_status csa2_get_device_status(void *stream, int32_t *code_out) {
   if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(v)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (v != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero)) != cudaSuccess)
     return CSA2_ERR_CUDA;
+  uint32_t kv8_word = 0;
+  const csa2_status rc = kv8_take_status(&kv8_word);
+  if (rc != CSA2_OK) return rc;
+  v |= kv8_word;
   if (code_out) *code_out = (int32_t)v;
   return v ? CSA2_ERR_DEVICE_STATUS : CSA2_OK;
 }

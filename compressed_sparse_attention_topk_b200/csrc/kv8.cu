@@ -1,0 +1,238 @@
+// C ABI of the 8-bit paged key/value cache (see include/csa2.h).  A
+// translation unit of its own, with a device status word of its own:
+// csa2_get_device_status reports both.
+#include "csa2.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "host.cuh"
+#include "kv8_attn.cuh"
+#include "kv8_cache.cuh"
+#include "kv8_select.cuh"
+
+namespace csa2 {
+
+// Reads and clears this unit's device status word (the stream has been
+// synchronised).
+csa2_status kv8_take_status(uint32_t *v) {
+  const uint32_t zero = 0;
+  *v = 0;
+  if (cudaMemcpyFromSymbol(v, g_device_status, sizeof(*v)) != cudaSuccess) return CSA2_ERR_CUDA;
+  if (*v && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero)) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  return CSA2_OK;
+}
+
+}  // namespace csa2
+
+using namespace csa2;
+
+namespace {
+
+int log2_of(int32_t block) {
+  return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : block == 128 ? 7 : -1;
+}
+
+// Checks a cache and makes the kernels' view of it.
+csa2_status cache_view(const csa2_kv8 *c, kv8::Cache *out) {
+  if (!c || c->Hk < 1 || c->D < 1 || c->block < 1 || c->pages < 1) return CSA2_ERR_INVALID_ARG;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->k_sum || !aligned(c->k, 16) ||
+      !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(c->k_sum, 16))
+    return CSA2_ERR_INVALID_ARG;
+  const int shift = log2_of(c->block);
+  if (shift < 0 || (c->D != 64 && c->D != 128) || c->Hk > 128 ||
+      c->pages >= (int64_t(1) << 31) / c->block / c->Hk)
+    return CSA2_ERR_UNSUPPORTED;
+  *out = {c->k,   c->v,     c->k_scale, c->v_scale, c->k_sum,
+          (int32_t)c->pages, c->Hk,    c->block,   shift,      c->D};
+  return CSA2_OK;
+}
+
+// Checks shared by the calls over a step's tokens (n > 0).
+csa2_status check_step(const uint16_t *q, int64_t q_stride, const kv8::Cache &c,
+                       const int32_t *table, int32_t width, const int32_t *cu,
+                       const int32_t *lens, int32_t B, int32_t H) {
+  if (!q || !table || !cu || !lens || !aligned(q, 16) || !aligned(table, 4) || !aligned(cu, 4) ||
+      !aligned(lens, 4) || width < 1 || H < 1 || H % c.Hk != 0 || q_stride % 8 != 0 ||
+      q_stride < int64_t(H) * c.D)
+    return CSA2_ERR_INVALID_ARG;
+  if (H > 128 || B > kv8::kMaxSeqs) return CSA2_ERR_UNSUPPORTED;
+  return CSA2_OK;
+}
+
+template <int D, int BS>
+void launch_append(const kv8::AppendParams &p, cudaStream_t st) {
+  const dim3 grid((unsigned)ceil_div(p.n, p.group), (unsigned)p.c.Hk, 2);
+  kv8::kv8_append_kernel<D, BS><<<grid, kv8::kAppendThreads, 0, st>>>(p);
+}
+
+template <int D>
+csa2_status launch_append_d(const kv8::AppendParams &p, cudaStream_t st) {
+  switch (p.c.bs) {
+    case 16: launch_append<D, 16>(p, st); break;
+    case 32: launch_append<D, 32>(p, st); break;
+    case 64: launch_append<D, 64>(p, st); break;
+    default: launch_append<D, 128>(p, st); break;
+  }
+  return after_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+csa2_status csa2_block_tables(const int32_t *lens, const int32_t *add, int32_t B, int32_t block,
+                              int32_t *table, int32_t width, const int32_t *free_pages,
+                              int32_t n_free, int32_t *lens_out, int32_t *cu, int64_t *slots,
+                              int32_t *pos, int64_t cap, int32_t *used, void *stream) {
+  if (B < 0 || width < 1 || n_free < 0 || cap < 0 || block < 1) return CSA2_ERR_INVALID_ARG;
+  if (!cu || !used || (B > 0 && (!lens || !add || !table || !lens_out)) ||
+      (n_free > 0 && !free_pages) || (cap > 0 && (!slots || !pos)) || (B > 0 && lens_out == lens) ||
+      !aligned(lens, 4) || !aligned(add, 4) || !aligned(table, 4) || !aligned(free_pages, 4) ||
+      !aligned(lens_out, 4) || !aligned(cu, 4) || !aligned(used, 4) || !aligned(slots, 8) ||
+      !aligned(pos, 4))
+    return CSA2_ERR_INVALID_ARG;
+  const int shift = log2_of(block);
+  if (shift < 0 || B > kv8::kMaxSeqs || int64_t(width) * block >= (int64_t(1) << 31) ||
+      cap >= (int64_t(1) << 31))
+    return CSA2_ERR_UNSUPPORTED;
+  const kv8::TableParams p{lens, add, table, free_pages, lens_out, cu,    slots, pos,
+                           used, cap, B,     shift,      width,    n_free};
+  const int64_t blocks = std::min<int64_t>(
+      std::max<int64_t>({1, ceil_div(cap, kv8::kTableThreads), ceil_div(B, 64)}), device_sms());
+  TraceScope ts("block_tables", as_stream(stream));
+  kv8::block_tables_kernel<<<(unsigned)blocks, kv8::kTableThreads, (2 * size_t(B) + 1) * 4,
+                             as_stream(stream)>>>(p);
+  return after_launch();
+}
+
+csa2_status csa2_kv8_append(const csa2_kv8 *cache, const uint16_t *k_new, int64_t k_stride,
+                            const uint16_t *v_new, int64_t v_stride, const int64_t *slots,
+                            int64_t n, void *stream) {
+  kv8::AppendParams p{};
+  csa2_status rc = cache_view(cache, &p.c);
+  if (rc != CSA2_OK) return rc;
+  if (n < 0) return CSA2_ERR_INVALID_ARG;
+  if (n == 0) return CSA2_OK;
+  const int64_t row = int64_t(p.c.Hk) * p.c.D;
+  if (!k_new || !v_new || !slots || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+      !aligned(slots, 8) || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < row ||
+      v_stride < row)
+    return CSA2_ERR_INVALID_ARG;
+  if (n >= (int64_t(1) << 31)) return CSA2_ERR_UNSUPPORTED;
+  p.x[0] = k_new;
+  p.x[1] = v_new;
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.slots = slots;
+  p.n = n;
+  p.group = n <= 1024 ? 1 : 16;
+  TraceScope ts("kv8_append", as_stream(stream));
+  return p.c.D == 64 ? launch_append_d<64>(p, as_stream(stream))
+                     : launch_append_d<128>(p, as_stream(stream));
+}
+
+csa2_status csa2_kv8_unpack(const csa2_kv8 *cache, const int64_t *slots, int64_t n, float *k_out,
+                            float *v_out, void *stream) {
+  kv8::Cache c;
+  csa2_status rc = cache_view(cache, &c);
+  if (rc != CSA2_OK) return rc;
+  if (n < 0 || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 8))
+    return CSA2_ERR_INVALID_ARG;
+  if (n == 0 || (!k_out && !v_out)) return CSA2_OK;
+  if (!slots) return CSA2_ERR_INVALID_ARG;
+  const int64_t units = n * c.Hk * (c.D / 16);
+  const int64_t blocks = std::min<int64_t>(ceil_div(units, 256), int64_t(device_sms()) * 8);
+  TraceScope ts("kv8_unpack", as_stream(stream));
+  kv8::kv8_unpack_kernel<<<dim3((unsigned)blocks, 2), 256, 0, as_stream(stream)>>>(c, slots, n,
+                                                                                  k_out, v_out);
+  return after_launch();
+}
+
+size_t csa2_kv8_select_workspace_size(int64_t n, int32_t Hk, int32_t width) {
+  if (n < 0 || Hk < 1 || Hk > 128 || width < 1 || width > 65536) return 0;
+  return std::max<size_t>(256, align_up(size_t(n) * Hk * width * 4, 256));
+}
+
+csa2_status csa2_kv8_select(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
+                            const int32_t *table, int32_t width, const int32_t *cu,
+                            const int32_t *lens, int32_t B, int64_t n, int32_t H, int32_t n_sel,
+                            int32_t n_first, int32_t n_last, int32_t *sel, void *ws,
+                            size_t ws_bytes, void *stream) {
+  kv8::SelectParams p{};
+  csa2_status rc = cache_view(cache, &p.c);
+  if (rc != CSA2_OK) return rc;
+  if (n < 0 || B < 0 || n_sel < 1 || n_first < 0 || n_last < 1 ||
+      int64_t(n_first) + n_last > n_sel)
+    return CSA2_ERR_INVALID_ARG;
+  if (n == 0 || B == 0) return CSA2_OK;
+  rc = check_step(q, q_stride, p.c, table, width, cu, lens, B, H);
+  if (rc != CSA2_OK) return rc;
+  if (!sel || !aligned(sel, 4)) return CSA2_ERR_INVALID_ARG;
+  if (n_sel > 4096 || width > 65536 || n >= (int64_t(1) << 31)) return CSA2_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < csa2_kv8_select_workspace_size(n, p.c.Hk, width) || !aligned(ws, 16))
+    return CSA2_ERR_WORKSPACE;
+  p.s = {cu, lens, table, B, width, n};
+  p.q = q;
+  p.q_stride = q_stride;
+  p.G = H / p.c.Hk;
+  p.n_sel = n_sel;
+  p.n_first = n_first;
+  p.n_last = n_last;
+  p.sel = sel;
+  p.scores = static_cast<float *>(ws);
+  const dim3 grid((unsigned)std::min<int64_t>(n, 65535), (unsigned)p.c.Hk);
+  TraceScope ts("kv8_select", as_stream(stream));
+  kv8::kv8_select_kernel<<<grid, kv8::kSelectThreads, 0, as_stream(stream)>>>(p);
+  return after_launch();
+}
+
+size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk, int32_t D,
+                                    int32_t n_sel) {
+  if (n < 0 || B < 0 || H < 1 || Hk < 1 || H % Hk != 0 || (D != 64 && D != 128) || n_sel < 0)
+    return 0;
+  return 256;
+}
+
+csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
+                          const int32_t *table, int32_t width, const int32_t *cu,
+                          const int32_t *lens, int32_t B, int64_t n, int32_t H,
+                          const int32_t *sel, int32_t n_sel, float sm_scale, uint16_t *out,
+                          float *lse, void *ws, size_t ws_bytes, void *stream) {
+  kv8::AttnParams p{};
+  csa2_status rc = cache_view(cache, &p.c);
+  if (rc != CSA2_OK) return rc;
+  if (n < 0 || B < 0 || n_sel < 0 || (sel != nullptr) != (n_sel > 0) || !std::isfinite(sm_scale))
+    return CSA2_ERR_INVALID_ARG;
+  if (n == 0 || B == 0) return CSA2_OK;
+  rc = check_step(q, q_stride, p.c, table, width, cu, lens, B, H);
+  if (rc != CSA2_OK) return rc;
+  if (!out || !aligned(out, 16) || !aligned(lse, 4) || !aligned(sel, 4))
+    return CSA2_ERR_INVALID_ARG;
+  if (n_sel > 65536 || n >= (int64_t(1) << 31) / H) return CSA2_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < csa2_kv8_attn_workspace_size(n, B, H, p.c.Hk, p.c.D, n_sel) ||
+      !aligned(ws, 16))
+    return CSA2_ERR_WORKSPACE;
+  p.s = {cu, lens, table, B, width, n};
+  p.q = q;
+  p.q_stride = q_stride;
+  p.G = H / p.c.Hk;
+  p.sel = sel;
+  p.n_sel = n_sel;
+  p.sm_scale = sm_scale;
+  p.out = out;
+  p.lse = lse;
+  const unsigned blocks = (unsigned)ceil_div(n * H, 4);
+  TraceScope ts("kv8_attn", as_stream(stream));
+  if (p.c.D == 64)
+    kv8::kv8_attn_kernel<64><<<blocks, 128, 0, as_stream(stream)>>>(p);
+  else
+    kv8::kv8_attn_kernel<128><<<blocks, 128, 0, as_stream(stream)>>>(p);
+  return after_launch();
+}
+
+}  // extern "C"

@@ -1,0 +1,363 @@
+// The 8-bit paged key/value cache: block tables and slot maps, the writer,
+// the reader (contracts in include/csa2.h).
+#pragma once
+
+#include "common.cuh"
+
+namespace csa2 {
+namespace kv8 {
+
+constexpr uint32_t kStatusBadLength = 4u;  // block tables: bad length, or no page or room
+constexpr int kMaxSeqs = 4096;
+
+struct Cache {
+  int8_t *k, *v;
+  float *k_scale, *v_scale;
+  int16_t *k_sum;
+  int32_t pages, Hk, bs, bs_shift, D;
+};
+
+// ---------------------------------------------------------------------------
+// Block tables and slot maps.
+//
+// Two prefix sums over the requests (tokens added, pages taken), then a
+// gather per token and a copy per new page.  Latency-bound: B <= 4096 lengths
+// are 32 KB, so every CTA repeats the scan (L2 reads) instead of waiting for
+// another one's, and the tokens are dealt over the CTAs.
+// ---------------------------------------------------------------------------
+constexpr int kTableThreads = 512;
+
+struct TableParams {
+  const int32_t *lens, *add;
+  int32_t *table;
+  const int32_t *free_pages;
+  int32_t *lens_out, *cu;
+  int64_t *slots;
+  int32_t *pos, *used;
+  int64_t cap;
+  int32_t B, bs_shift, width, n_free;
+};
+
+__device__ __forceinline__ long long warp_incl_scan64(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int32_t sat32(long long v) {
+  return v > 0x7fffffffll ? 0x7fffffff : (int32_t)v;
+}
+
+__global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const TableParams p) {
+  // per request: first token and first page taken, then totals
+  extern __shared__ int32_t table_smem[];
+  int32_t *s_cu = table_smem, *s_page = table_smem + p.B + 1;
+  __shared__ long long s_warp[2][kTableThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bs1 = (1 << p.bs_shift) - 1;
+  bool bad = false;
+  long long run_t = 0, run_p = 0;  // totals of the chunks before this one
+  for (int b0 = 0; b0 < p.B; b0 += kTableThreads) {
+    const int b = b0 + tid;
+    long long len = 0, add = 0;
+    if (b < p.B) {
+      len = p.lens[b];
+      add = p.add[b];
+      bad |= len < 0 || add < 0;
+      len = len < 0 ? 0 : len;
+      add = add < 0 ? 0 : add;
+    }
+    const long long have = min64((len + bs1) >> p.bs_shift, p.width);
+    const long long need = min64((len + add + bs1) >> p.bs_shift, p.width);
+    const long long it = warp_incl_scan64(add), ip = warp_incl_scan64(need - have);
+    if (lane == 31) {
+      s_warp[0][warp] = it;
+      s_warp[1][warp] = ip;
+    }
+    __syncthreads();
+    long long bt = run_t, bp = run_p;
+    for (int w = 0; w < kTableThreads / 32; ++w) {
+      if (w < warp) {
+        bt += s_warp[0][w];
+        bp += s_warp[1][w];
+      }
+      run_t += s_warp[0][w];
+      run_p += s_warp[1][w];
+    }
+    if (b < p.B) {
+      s_cu[b] = sat32(bt + it - add);
+      s_page[b] = sat32(bp + ip - (need - have));
+      if (blockIdx.x == 0) {
+        p.lens_out[b] = sat32(len + add);
+        p.cu[b] = sat32(bt + it - add);
+      }
+    }
+    __syncthreads();
+  }
+  const int32_t total = sat32(run_t);
+  if (tid == 0) {
+    s_cu[p.B] = total;
+    if (blockIdx.x == 0) {
+      p.cu[p.B] = total;
+      p.used[0] = sat32(run_p);
+      bad |= run_t > p.cap || run_p > p.n_free;
+    }
+  }
+  __syncthreads();
+
+  // new pages: one warp per request
+  const int nwarps = gridDim.x * (kTableThreads / 32);
+  for (int b = blockIdx.x * (kTableThreads / 32) + warp; b < p.B; b += nwarps) {
+    const long long len = max(p.lens[b], 0);
+    const long long end = len + max(p.add[b], 0);
+    const int have = (int)min64((len + bs1) >> p.bs_shift, p.width);
+    const int need = (int)min64((end + bs1) >> p.bs_shift, p.width);
+    bad |= ((end + bs1) >> p.bs_shift) > p.width;
+    for (int j = have + lane; j < need; j += 32) {
+      const long long f = (long long)s_page[b] + j - have;
+      p.table[(int64_t)b * p.width + j] = f < p.n_free ? p.free_pages[f] : -1;
+    }
+  }
+  // tokens
+  const int64_t step = (int64_t)gridDim.x * kTableThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kTableThreads + tid; i < p.cap; i += step) {
+    int64_t slot = -1;
+    int32_t at = -1;
+    if (i < total) {
+      int lo = 0, hi = p.B;  // s_cu[lo] <= i < s_cu[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_cu[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      const long long len = max(p.lens[lo], 0);
+      const long long pos = len + (i - s_cu[lo]);
+      const long long j = pos >> p.bs_shift;
+      const long long have = min64((len + bs1) >> p.bs_shift, p.width);
+      int32_t page = -1;
+      if (j < have) {
+        page = p.table[(int64_t)lo * p.width + j];
+      } else if (j < p.width) {
+        const long long f = (long long)s_page[lo] + j - have;
+        if (f < p.n_free) page = p.free_pages[f];
+      }
+      if (page >= 0) slot = ((int64_t)page << p.bs_shift) + (pos & bs1);
+      at = sat32(pos);
+    }
+    p.slots[i] = slot;
+    p.pos[i] = at;
+  }
+  if (bad) raise_status(kStatusBadLength);
+}
+
+// ---------------------------------------------------------------------------
+// The writer.
+//
+// A run is the tokens of one page in a call: consecutive tokens at ascending
+// slots.  One CTA per (group of tokens, kv head, keys or values) looks for
+// the runs that begin in its group and, for each, keeps the run's rows in
+// registers (read once) while it takes their largest magnitude, settles the
+// page's scale, requantises the earlier rows if it grew, and writes the new
+// codes; for keys it also forms the page's code sums, so earlier rows are
+// read anyway.  Bound by bytes (4 D read + 2 D written per token and head).
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 128;
+
+struct AppendParams {
+  Cache c;
+  const uint16_t *x[2];
+  int64_t stride[2];
+  const int64_t *slots;
+  int64_t n;
+  int32_t group;  // tokens per CTA
+};
+
+__device__ __forceinline__ int8_t kv8_code(float x, float s) {
+  const int q = __float2int_rn(__fdiv_rn(x, s));
+  return (int8_t)max(-127, min(127, q));
+}
+
+template <int D, int BS>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendParams p) {
+  constexpr int CPR = D / 8;                    // 8-element pieces of a row
+  constexpr int RPP = kAppendThreads / CPR;     // rows per pass
+  constexpr int PASSES = (BS + RPP - 1) / RPP;
+  __shared__ float s_max[kAppendThreads / 32];
+  __shared__ int s_len;
+  __shared__ int32_t s_sum[RPP][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.y, vals = blockIdx.z;
+  const int col = (tid % CPR) * 8, rsub = tid / CPR;
+  const int64_t slots_end = (int64_t)p.c.pages * BS;
+  const int64_t g0 = (int64_t)blockIdx.x * p.group;
+  const int64_t g1 = min64(g0 + p.group, p.n);
+  for (int64_t i = g0; i < g1; ++i) {
+    const int64_t slot = p.slots[i];
+    if (slot < 0) continue;
+    if (slot >= slots_end) {
+      if (tid == 0) raise_status(kStatusBadIndex);
+      continue;
+    }
+    const int r0 = (int)(slot & (BS - 1));
+    if (i > 0 && r0 != 0 && p.slots[i - 1] == slot - 1) continue;  // inside an earlier run
+    // run length: the first row that does not follow
+    if (tid == 0) s_len = BS - r0;
+    __syncthreads();
+    if (tid < BS - r0 && (i + tid >= p.n || p.slots[i + tid] != slot + tid))
+      atomicMin(&s_len, tid);
+    __syncthreads();
+    const int m = s_len;
+    const int64_t page = slot / BS;
+    const int64_t ph = page * p.c.Hk + h;
+    int8_t *codes = (vals ? p.c.v : p.c.k) + ph * BS * D;
+    float *scale_at = (vals ? p.c.v_scale : p.c.k_scale) + ph;
+    const float s_old = r0 ? *scale_at : 0.f;
+    const uint16_t *src = p.x[vals] + i * p.stride[vals] + (int64_t)h * D + col;
+
+    uint4 x[PASSES];
+    float big = 0.f;
+#pragma unroll
+    for (int a = 0; a < PASSES; ++a) {
+      const int r = a * RPP + rsub;
+      x[a] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < m) x[a] = *reinterpret_cast<const uint4 *>(src + r * p.stride[vals]);
+    }
+#pragma unroll
+    for (int a = 0; a < PASSES; ++a) {
+      const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        big = fmaxf(big, fabsf(__uint_as_float(w[e] << 16)));
+        big = fmaxf(big, fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+      }
+    }
+    big = warp_max(big);
+    if (lane == 0) s_max[warp] = big;
+    __syncthreads();  // (also: every thread has read the old scale)
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) big = fmaxf(big, s_max[w]);
+    const float s = fmaxf(s_old, __fdiv_rn(big, 127.f));
+    if (tid == 0) *scale_at = s;
+
+    int32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const bool grew = s > s_old;
+    if (grew || !vals) {  // earlier rows: requantised, and summed for the keys
+      const float ratio = grew ? __fdiv_rn(s_old, s) : 1.f;
+      for (int r = rsub; r < r0; r += RPP) {
+        uint2 *at = reinterpret_cast<uint2 *>(codes + r * D + col);
+        const uint2 w = *at;
+        uint32_t o[2] = {w.x, w.y};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          int c = (int8_t)(o[e >> 2] >> (8 * (e & 3)));
+          if (grew) {
+            c = __float2int_rn(__fmul_rn((float)c, ratio));
+            o[e >> 2] = (o[e >> 2] & ~(0xffu << (8 * (e & 3)))) |
+                        ((uint32_t)(uint8_t)c << (8 * (e & 3)));
+          }
+          sum[e] += c;
+        }
+        if (grew) *at = make_uint2(o[0], o[1]);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < PASSES; ++a) {
+      const int r = a * RPP + rsub;
+      if (r >= m) continue;
+      const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+      uint32_t o[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t bits = (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16);
+        const int c = s > 0.f ? kv8_code(__uint_as_float(bits), s) : 0;
+        o[e >> 2] |= (uint32_t)(uint8_t)c << (8 * (e & 3));
+        sum[e] += c;
+      }
+      *reinterpret_cast<uint2 *>(codes + (r0 + r) * D + col) = make_uint2(o[0], o[1]);
+    }
+    if (!vals) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_sum[rsub][col + e] = sum[e];
+      __syncthreads();
+      if (tid < D) {
+        int32_t t = 0;
+#pragma unroll
+        for (int r = 0; r < RPP; ++r) t += s_sum[r][tid];
+        p.c.k_sum[ph * D + tid] = (int16_t)t;
+      }
+    }
+    __syncthreads();  // s_len, s_max and s_sum are free again
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The reader: one thread per 16 codes.  Bound by bytes (D read and 4 D
+// written per row, head and array).
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) kv8_unpack_kernel(const Cache c,
+                                                         const int64_t *__restrict__ slots,
+                                                         int64_t n, float *k_out, float *v_out) {
+  const int cpr = c.D / 16;
+  const int64_t per = (int64_t)c.Hk * cpr;
+  const int64_t units = n * per;
+  const int8_t *codes = blockIdx.y ? c.v : c.k;
+  const float *scales = blockIdx.y ? c.v_scale : c.k_scale;
+  float *out = blockIdx.y ? v_out : k_out;
+  if (!out) return;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units; u += step) {
+    const int64_t i = u / per;
+    const int rest = (int)(u - i * per);
+    const int h = rest / cpr, piece = rest - h * cpr;
+    const int64_t slot = slots[i];
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    float s = 0.f;
+    if (slot >= ((int64_t)c.pages << c.bs_shift)) {
+      if (rest == 0) raise_status(kStatusBadIndex);
+    } else if (slot >= 0) {
+      const int64_t ph = (slot >> c.bs_shift) * c.Hk + h;
+      const int64_t row = (ph << c.bs_shift) + (slot & (c.bs - 1));
+      w = *reinterpret_cast<const uint4 *>(codes + row * c.D + piece * 16);
+      s = scales[ph];
+    }
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    float4 *dst = reinterpret_cast<float4 *>(out + u * 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float4 f;
+      f.x = __fmul_rn((float)(int8_t)(ws[q]), s);
+      f.y = __fmul_rn((float)(int8_t)(ws[q] >> 8), s);
+      f.z = __fmul_rn((float)(int8_t)(ws[q] >> 16), s);
+      f.w = __fmul_rn((float)(int8_t)(ws[q] >> 24), s);
+      dst[q] = f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sequences of a step.
+// ---------------------------------------------------------------------------
+struct Steps {
+  const int32_t *cu, *lens, *table;
+  int32_t B, width;
+  int64_t n;
+};
+
+// The sequence that owns token i (cu[b] <= i < cu[b+1]), or -1 for padding.
+__device__ __forceinline__ int seq_of(const Steps &s, int64_t i) {
+  if (s.B == 0 || i >= s.cu[s.B]) return -1;
+  int lo = 0, hi = s.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.cu[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace kv8
+}  // namespace csa2

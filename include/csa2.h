@@ -434,6 +434,142 @@ csa2_status csa2_layer_group_run(const csa2_layer_mode *modes, const csa2_layer_
                                  const csa2_dims *dims, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* 8-bit paged key/value cache                                             */
+/* ---------------------------------------------------------------------- */
+
+/* A per-head key/value cache in pages, for layers that keep every token
+ * instead of compressed entries.  The pages describe no such cache ("an entry
+ * serves all heads" is theirs, see csa2_sparse_attn_decode); it is the
+ * library's own.  A page holds `block` consecutive tokens of one sequence,
+ * for every kv head, as int8 codes with one fp32 scale per page and head for
+ * the keys and one for the values: value = code * scale.  k_sum is the page's
+ * cheap summary: the sum of its key codes, which csa2_kv8_select scores.
+ *   k, v     device, int8 [pages, Hk, block, D]      (16-byte aligned)
+ *   k_scale, v_scale  device, fp32 [pages, Hk], finite and >= 0
+ *   k_sum    device, int16 [pages, Hk, D]            (16-byte aligned)
+ * Supported: block in {16, 32, 64, 128}, D in {64, 128}, 1 <= Hk <= 128,
+ * pages >= 1, pages * Hk * block < 2^31.
+ *
+ * Sequences: a step brings n tokens of B sequences.  Sequence b owns tokens
+ * cu[b] .. cu[b+1]-1 (cu[0] = 0, ascending; device int32 [B+1]) and has
+ * lens[b] tokens in the cache, the step's own among them (device int32 [B]),
+ * so its token i sits at position lens[b] - cu[b+1] + i.  table (device
+ * int32 [B, width]) names the page of each of its blocks; entries past the
+ * last block are not read.  Tokens past cu[B] belong to nobody (padding):
+ * their rows of every output are left as they were.  A page outside the
+ * cache, or a block past the table's width, is skipped (its tokens are not
+ * seen) and recorded in the device status word (bit 0).
+ *
+ * Token arrays (q, k_new, v_new) are bf16 [n, heads, D] with the heads of a
+ * token dense and a stride of their own between tokens (in elements, a
+ * multiple of 8), so they may be slices of one projection's output. */
+typedef struct csa2_kv8 {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    int16_t *k_sum;
+    int64_t pages;
+    int32_t Hk, block, D;
+} csa2_kv8;
+
+/* Block tables and slot maps of a step, from request lengths.  Request b
+ * holds lens[b] tokens in ceil(lens[b] / block) pages and adds add[b]; each
+ * request in turn takes the further pages it needs from the front of the
+ * free list.
+ *   lens, add   device, int32 [B]     (a negative value counts as 0, and is
+ *               recorded in the device status word, bit 2)
+ *   table       device, int32 [B, width]: the new pages' entries are written
+ *   free_pages  device, int32 [n_free]
+ *   lens_out    device, int32 [B]     lens + add (must not be lens itself)
+ *   cu          device, int32 [B+1]   token offsets of the requests
+ *   slots       device, int64 [cap]   page * block + row of every token of the
+ *               step, in request order; -1 from the last token on
+ *   pos         device, int32 [cap]   its position; -1 from the last token on
+ *   used        device, int32 [1]     pages taken from the free list
+ * When the free list is too short, or a request outgrows its table row, the
+ * tokens without a page get slot -1 and the entries without one -1; tokens
+ * past cap are not written; each is recorded in the status word (bit 2), and
+ * `used` still counts what was asked for.
+ * Supported: 0 <= B <= 4096, width * block < 2^31, cap < 2^31. */
+csa2_status csa2_block_tables(const int32_t *lens, const int32_t *add, int32_t B, int32_t block,
+                              int32_t *table, int32_t width, const int32_t *free_pages,
+                              int32_t n_free, int32_t *lens_out, int32_t *cu, int64_t *slots,
+                              int32_t *pos, int64_t cap, int32_t *used, void *stream);
+
+/* Write n tokens' keys and values at their slots (page * block + row; a
+ * negative slot writes nothing, one past the cache is skipped and recorded,
+ * bit 0).  Tokens of one page are consecutive in the call, at ascending rows
+ * (as csa2_block_tables lays them out); two runs of tokens in one page, or a
+ * slot twice, leave that page's contents unspecified.  Per run, head and
+ * array: s' = max(s, amax / 127) with s the page's scale (0 when the run
+ * starts at row 0: a page begun anew) and amax the run's largest |x|; when
+ * s' > s the codes of the rows before the run become rint(c * (s / s'));
+ * the run's codes are rint(x / s') (0 when s' is 0), within +-127; fp32
+ * operations rounded on their own, rint to even.  k_sum becomes the sum of
+ * the key codes of the rows up to the run's last.  Rows behind it stay.
+ *   k_new, v_new  device, bf16 [n, Hk, D], finite, strides in elements
+ *   slots         device, int64 [n] */
+csa2_status csa2_kv8_append(const csa2_kv8 *cache, const uint16_t *k_new, int64_t k_stride,
+                            const uint16_t *v_new, int64_t v_stride, const int64_t *slots,
+                            int64_t n, void *stream);
+
+/* Read rows back: k_out, v_out fp32 [n, Hk, D] = code * scale of the rows at
+ * slots (int64 [n]); zeros for a negative slot, and for one past the cache
+ * (recorded, bit 0).  Either output may be NULL. */
+csa2_status csa2_kv8_unpack(const csa2_kv8 *cache, const int64_t *slots, int64_t n, float *k_out,
+                            float *v_out, void *stream);
+
+/* Workspace bytes of csa2_kv8_select (0 on invalid sizes). */
+size_t csa2_kv8_select_workspace_size(int64_t n, int32_t Hk, int32_t width);
+
+/* The blocks that each token attends to, by a cheap score of every block it
+ * sees.  For token i at position p and kv head h, over the blocks j = 0 ..
+ * p / block: qs = the sum of the G = H / Hk query heads of the group, in
+ * fp32 (from a sum in 64 bits); q8 = rint(qs * (127 / max |qs|)), 0 when the
+ * maximum is 0 or not finite; score_j = fp32(sum_d q8[d] * k_sum[j][h][d]) *
+ * k_scale[j][h], fp32 operations rounded on their own.  Kept: the first
+ * n_first and the last n_last of the blocks, then the highest scores of the
+ * others up to n_sel in all, ties to the lower block.
+ *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
+ *   sel  device, int32 [n, Hk, n_sel] (output): blocks ascending, then -1
+ *   ws   device workspace of ws_bytes >= csa2_kv8_select_workspace_size
+ * A block whose page is outside the cache scores lowest of all.
+ * Supported: H a multiple of Hk, H <= 128, 1 <= n_sel <= 4096, n_first >= 0,
+ * n_last >= 1 (the block being filled is always kept), n_first + n_last <=
+ * n_sel, width <= 65536, B <= 4096. */
+csa2_status csa2_kv8_select(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
+                            const int32_t *table, int32_t width, const int32_t *cu,
+                            const int32_t *lens, int32_t B, int64_t n, int32_t H, int32_t n_sel,
+                            int32_t n_first, int32_t n_last, int32_t *sel, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/* Workspace bytes of csa2_kv8_attn on the current device (0 on invalid
+ * sizes). */
+size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk, int32_t D,
+                                    int32_t n_sel);
+
+/* Causal attention over the cache.  Token i at position p, query head h (kv
+ * head h / (H / Hk)): softmax over the logits sm_scale * <q, key> of the
+ * positions 0 .. p of its sequence -- or, with sel, of those of them in its
+ * listed blocks -- of values code * scale.  out = sum p * value rounded to
+ * bf16 once, lse = natural log of sum exp(logit).  A token that sees nothing
+ * (no position, an empty list, only skipped pages) gets out = 0, lse = -inf.
+ * A sequence with more new tokens than lens has tokens at negative positions,
+ * which see nothing.
+ *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
+ *   sel  device, int32 [n, Hk, n_sel] or NULL (n_sel 0): block numbers of the
+ *        sequence, each at most once, a negative one is skipped
+ *   out  device, bf16 [n, H, D] (16-byte aligned); lse device, fp32 [n, H] or
+ *        NULL
+ *   ws   device workspace of ws_bytes >= csa2_kv8_attn_workspace_size
+ * Supported: H a multiple of Hk, H <= 128, n_sel <= 65536, B <= 4096,
+ * sm_scale finite. */
+csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
+                          const int32_t *table, int32_t width, const int32_t *cu,
+                          const int32_t *lens, int32_t B, int64_t n, int32_t H,
+                          const int32_t *sel, int32_t n_sel, float sm_scale, uint16_t *out,
+                          float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Staging copies                                                          */
 /* ---------------------------------------------------------------------- */
 
@@ -524,8 +660,10 @@ csa2_status csa2_wait_timeout_selftest(int64_t limit_cycles, void *stream);
 
 /* Synchronise `stream`, then read and clear the current device's status
  * word.  *code_out (may be NULL) receives the raw word: 0 = clean, bit 0 =
- * an attention index >= N was skipped, bit 1 = a pipeline wait gave up
- * after its iteration limit.  Returns CSA2_ERR_DEVICE_STATUS when the word
+ * an index outside its store (an entry >= N, a page or slot outside the
+ * cache) was skipped, bit 1 = a pipeline wait gave up after its iteration
+ * limit, bit 2 = csa2_block_tables met a negative length, or had no page or
+ * no room for a token.  Returns CSA2_ERR_DEVICE_STATUS when the word
  * was non-zero, CSA2_ERR_CUDA when the synchronisation failed. */
 csa2_status csa2_get_device_status(void *stream, int32_t *code_out);
 
