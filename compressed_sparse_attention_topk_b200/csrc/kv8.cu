@@ -4,6 +4,7 @@
 #include "csa2.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -79,6 +80,77 @@ csa2_status launch_append_d(const kv8::AppendParams &p, cudaStream_t st) {
     default: launch_append<D, 128>(p, st); break;
   }
   return after_launch();
+}
+
+// Kernels of an attention call and their workspace.
+struct AttnPlan {
+  int MT;          // 16-row tiles of a CTA's query rows
+  int ctas;
+  size_t part_at;  // the partials, behind one record per CTA
+  size_t bytes;
+};
+
+// 16 query rows per tile, or 32 where a sequence (or, with lists, a token)
+// has more on average: a second 16-row tile reads the same fragments of the
+// cache.
+AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
+  AttnPlan a{};
+  const int64_t rows = n_sel > 0 ? G : ceil_div(n * G, std::max(B, 1));
+  a.MT = rows > 16 ? 2 : 1;
+  a.ctas = 2 * device_sms();
+  a.part_at = align_up(size_t(a.ctas) * sizeof(int4), 256);
+  a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * 16 * a.MT * (D + 2) * 4, 256);
+  return a;
+}
+
+template <int D, int MT, bool P16>
+csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+  using S = kv8::SplitShape<D, MT>;
+  static std::atomic<bool> done[256];  // per device: attributes set
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 256 || !done[dev].load(std::memory_order_acquire)) {
+    if (set_smem_attr(kv8::kv8_split_kernel<D, MT, P16>, S::SMEM, false) != CSA2_OK)
+      return CSA2_ERR_CUDA;
+    if (dev >= 0 && dev < 256) done[dev].store(true, std::memory_order_release);
+  }
+  const uint64_t rows = uint64_t(p.c.pages) * p.c.Hk * p.c.bs;
+  const uint32_t box = P16 ? 16 : kv8::kUnit;
+  CUtensorMap km, vm;
+  if (!make_map_u8(&km, p.c.k, D, rows, 1, D, rows * D, box, 1) ||
+      !make_map_u8(&vm, p.c.v, D, rows, 1, D, rows * D, box, 1))
+    return CSA2_ERR_CUDA;
+  {
+    TraceScope ts("kv8_attn_split", st);
+    kv8::kv8_split_kernel<D, MT, P16>
+        <<<(unsigned)a.ctas, kv8::kSplitThreads, S::SMEM, st>>>(km, vm, p);
+    const csa2_status rc = after_launch();
+    if (rc != CSA2_OK) return rc;
+  }
+  TraceScope ts("kv8_attn_merge", st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.ctas, S::ROWS / 4);
+  cfg.blockDim = dim3(kv8::kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv8::kv8_merge_kernel<D, MT>, p, a.ctas) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  return after_launch();
+}
+
+template <int D>
+csa2_status launch_attn_d(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+  if (p.c.bs == 16)
+    return a.MT == 1 ? launch_split<D, 1, true>(p, a, st) : launch_split<D, 2, true>(p, a, st);
+  return a.MT == 1 ? launch_split<D, 1, false>(p, a, st) : launch_split<D, 2, false>(p, a, st);
+}
+
+csa2_status launch_attn(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+  return p.c.D == 64 ? launch_attn_d<64>(p, a, st) : launch_attn_d<128>(p, a, st);
 }
 
 }  // namespace
@@ -195,7 +267,7 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
                                     int32_t n_sel) {
   if (n < 0 || B < 0 || H < 1 || Hk < 1 || H % Hk != 0 || (D != 64 && D != 128) || n_sel < 0)
     return 0;
-  return 256;
+  return attn_plan(n, B, H / Hk, D, n_sel).bytes;
 }
 
 csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
@@ -213,7 +285,9 @@ csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *c
   if (rc != CSA2_OK) return rc;
   if (!out || !aligned(out, 16) || !aligned(lse, 4) || !aligned(sel, 4))
     return CSA2_ERR_INVALID_ARG;
-  if (n_sel > 65536 || n >= (int64_t(1) << 31) / H) return CSA2_ERR_UNSUPPORTED;
+  if (n_sel > 65536 || n >= (int64_t(1) << 31) / H ||
+      int64_t(width) * p.c.bs > kv8::kNoPos)
+    return CSA2_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < csa2_kv8_attn_workspace_size(n, B, H, p.c.Hk, p.c.D, n_sel) ||
       !aligned(ws, 16))
     return CSA2_ERR_WORKSPACE;
@@ -226,13 +300,10 @@ csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *c
   p.sm_scale = sm_scale;
   p.out = out;
   p.lse = lse;
-  const unsigned blocks = (unsigned)ceil_div(n * H, 4);
-  TraceScope ts("kv8_attn", as_stream(stream));
-  if (p.c.D == 64)
-    kv8::kv8_attn_kernel<64><<<blocks, 128, 0, as_stream(stream)>>>(p);
-  else
-    kv8::kv8_attn_kernel<128><<<blocks, 128, 0, as_stream(stream)>>>(p);
-  return after_launch();
+  const AttnPlan plan = attn_plan(n, B, p.G, p.c.D, n_sel);
+  p.rec = static_cast<int4 *>(ws);
+  p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + plan.part_at);
+  return launch_attn(p, plan, as_stream(stream));
 }
 
 }  // extern "C"

@@ -1,6 +1,20 @@
 // Attention over the 8-bit paged cache (contract of csa2_kv8_attn in
 // include/csa2.h).
+//
+// Mathematics, per query row (token, head) and page with scales ks, vs:
+//   x_j = (sm_scale log2(e) ks) <q, kcode_j>,  p_j = 2^(x_j - m),
+//   out = sum_j p_j vs vcode_j / sum_j p_j,   lse = ln 2 (m + log2 sum_j p_j)
+// in one pass over the keys with the running maximum m.  The codes are exact
+// in fp16, and so is q once its row is scaled by a power of two (its largest
+// magnitude goes to [1, 2); what is more than 2^-14 below it loses bits that
+// weigh less than fp32's in the dot), so the products are exact and their
+// sums fp32.  The weights are rounded once to fp16 as 2^14 p: 2^-11 of each
+// weight, and weights down to 2^-38 are not lost.  Sums of weights, maxima
+// and outputs stay in fp32; a page's scale multiplies its fp32 partial
+// output, so scales far apart lose nothing.
 #pragma once
+
+#include <cuda.h>
 
 #include "kv8_cache.cuh"
 
@@ -18,60 +32,694 @@ struct AttnParams {
   float sm_scale;
   uint16_t *out;        // [n, H, D]
   float *lse;           // [n, H] or null
+  float *part;          // split tiles: partial results, two per CTA
+  int4 *rec;            // split tiles: one record per CTA
 };
 
-// One warp per token and query head; a lane holds D / 32 dims.  One pass over
-// the keys with the running maximum and sum of the softmax in fp32.
-template <int D>
-__global__ void __launch_bounds__(128) kv8_attn_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t H = (int64_t)p.G * p.c.Hk;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t i = item / H;
-  const int head = (int)(item - i * H), h = head / p.G;
-  if (i >= p.s.n) return;
-  const int b = seq_of(p.s, i);
-  if (b < 0) return;
-  const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
-  float q[E], o[E];
-  for (int e = 0; e < E; ++e) {
-    q[e] = bf16_to_f32_bits(p.q[i * p.q_stride + (int64_t)head * D + lane * E + e]);
-    o[e] = 0.f;
+__device__ __forceinline__ void tma_load_rows(void *smem, const CUtensorMap *map, int row,
+                                              uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(smem_u32(smem)),
+      "l"(map), "r"(0), "r"(row), "r"(0), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+      "%9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bytes 0, 1 (hi = false) or 2, 3 of a word of codes with their sign bits
+// flipped (code + 128) -> two fp16 codes: 1024 + u by a byte permute, less 1152.
+template <bool HI>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
+  const uint32_t u = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), bias);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// ---------------------------------------------------------------------------
+// Few query rows per sequence (decode, drafts) or a list of blocks per token:
+// the work is the stream of the cache's bytes.
+//
+// A tile is 16 MT query rows (token-major, the group's heads inside) of one
+// sequence and kv head; its keys are cut into units of 32 positions.  The
+// units of all tiles form one line, cut evenly over the CTAs (lengths differ
+// by orders of magnitude between sequences), so a CTA works on the end of a
+// tile, whole tiles and the beginning of one; a tile that several CTAs share
+// leaves a partial (m, l, O) per CTA, merged in order by kv8_merge_kernel.
+// Within a CTA the warps take a tile's units in turn, each with its own ring
+// of units (TMA, one lane), its own softmax state and no barrier until the
+// tile's end: the 8-bit codes become fp16 fragments in registers (byte
+// permutes), and the products are mma.sync m16n8k16 -- with 16 or 32 rows
+// the tensor work is a fraction of the time the bytes take, and a 128-row
+// tcgen05 tile would be mostly padding.
+// ---------------------------------------------------------------------------
+constexpr int kSplitWarps = 4;
+constexpr int kSplitThreads = 32 * kSplitWarps;
+constexpr int kUnit = 32;
+constexpr int kStages = 3;
+constexpr int kNoPos = 1 << 30;  // a table reaches fewer positions; no row sees this one
+constexpr float kPBias = 14.f;  // weights are held as 2^14 p
+
+template <int D, int MT>
+struct SplitShape {
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int TILE = kUnit * D;                  // bytes of a unit's keys (or values)
+  static constexpr int RING = kStages * 2 * TILE;         // per warp
+  static constexpr int LDO = D + 4;                       // floats per row of a warp's result
+  static constexpr size_t SMEM = size_t(kSplitWarps) * RING + 1024;
+  static constexpr size_t PART = size_t(ROWS) * (D + 2);  // floats of one partial
+  static_assert(ROWS * LDO * 4 <= RING, "a warp's result reuses its ring");
+};
+
+// A tile: rows row0 .. row0 + nrows - 1 (row = token of the sequence * G +
+// head of the group).
+struct Tile {
+  int32_t b, h, row0, nrows, tok0;
+  int32_t pos0;      // position of the sequence's first new token
+  int32_t pos_first, pos_last;  // positions of the tile's first and last row
+  int32_t units;
+};
+
+// Work of sequence b: tiles per kv head and units per tile.
+template <int MT>
+__device__ __forceinline__ void seq_work(const AttnParams &p, int b, int &tiles, int &units,
+                                         int &t0, int &T, int &pos0) {
+  const int32_t lo = max(p.s.cu[b], 0), hi = p.s.cu[b + 1];
+  t0 = lo;
+  T = (int)max((int64_t)0, min64(hi, p.s.n) - lo);
+  const int64_t len = p.s.lens[b];
+  pos0 = (int)max((int64_t)-0x40000000, len - hi + lo);
+  tiles = (int)(((int64_t)T * p.G + 16 * MT - 1) / (16 * MT));
+  const int64_t reach = (int64_t)p.s.width << p.c.bs_shift;
+  const int64_t seen = min64(max(len, (int64_t)0), reach);
+  units = max(1, (int)((seen + kUnit - 1) / kUnit));
+}
+
+template <int D, int MT, bool P16>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    kv8_split_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
+  using S = SplitShape<D, MT>;
+  constexpr int NT = D / 8;    // output columns' n-tiles
+  constexpr int KS = D / 16;   // k-steps of a dot
+  extern __shared__ unsigned char split_smem[];
+  __shared__ uint64_t s_bar[kSplitWarps][kStages];
+  __shared__ float s_m[kSplitWarps][S::ROWS], s_l[kSplitWarps][S::ROWS];
+  __shared__ long long s_sum[kSplitWarps];
+  __shared__ long long s_pre;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  unsigned char *const ring0 = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(split_smem) + 1023) & ~uintptr_t(1023));
+  unsigned char *const ring = ring0 + warp * S::RING;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp][i], 1);
+    fence_barrier_init();
   }
-  float m = -INFINITY, l = 0.f;
-  const int64_t nblk = pos < 0 ? 0 : (pos >> p.c.bs_shift) + 1;
-  const int64_t count = p.sel ? p.n_sel : nblk;
-  for (int64_t x = 0; x < count; ++x) {
-    const int64_t j = p.sel ? p.sel[(i * p.c.Hk + h) * p.n_sel + x] : x;
-    if (j < 0 || j >= nblk) continue;
-    const int32_t page = j < p.s.width ? p.s.table[(int64_t)b * p.s.width + j] : -1;
-    if (page < 0 || page >= p.c.pages) {
-      if (lane == 0) raise_status(kStatusBadIndex);
-      continue;
+  pdl_allow_dependents();
+
+  // ---- the line of units: its length, and this CTA's stretch of it ----
+  long long W, u0, u1;
+  int b = 0;            // first tile's sequence (dense)
+  long long pre = 0;    // units before sequence b
+  const int xt = (p.G + S::ROWS - 1) / S::ROWS;  // tiles of a (token, kv head) with a list
+  const int list_units = P16 ? (p.n_sel + 1) / 2 : p.n_sel << (p.c.bs_shift - 5);
+  if (p.sel) {
+    const int64_t tokens = min64(p.s.n, p.s.cu[p.s.B]);
+    W = max((long long)tokens, 0ll) * p.c.Hk * xt * list_units;
+  } else {
+    long long mine = 0;
+    for (int i = tid; i < p.s.B; i += kSplitThreads) {
+      int tiles, units, t0, T, pos0;
+      seq_work<MT>(p, i, tiles, units, t0, T, pos0);
+      mine += (long long)tiles * units;
+      if (tiles > 0 && blockIdx.x == 0 &&
+          (int64_t)p.s.lens[i] > ((int64_t)p.s.width << p.c.bs_shift))
+        raise_status(kStatusBadIndex);
     }
-    const int64_t ph = (int64_t)page * p.c.Hk + h;
-    const float ks = p.c.k_scale[ph] * p.sm_scale, vs = p.c.v_scale[ph];
-    const int rows = (int)min64(p.c.bs, pos + 1 - (j << p.c.bs_shift));
-    for (int r = 0; r < rows; ++r) {
-      const int64_t at = ((ph << p.c.bs_shift) + r) * D + lane * E;
-      float dot = 0.f;
-      for (int e = 0; e < E; ++e) dot += q[e] * (float)p.c.k[at + e];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-      const float y = dot * ks;
-      const float mn = fmaxf(m, y);
-      const float corr = m == mn ? 1.f : expf(m - mn), w = expf(y - mn);
-      m = mn;
-      l = l * corr + w;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * corr + w * vs * (float)p.c.v[at + e];
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    W = 0;
+    for (int w = 0; w < kSplitWarps; ++w) W += s_sum[w];
+    W *= p.c.Hk;
+  }
+  // a CTA gets at least one unit per warp
+  const long long ctas = max(1ll, min((long long)gridDim.x, (W + kSplitWarps - 1) / kSplitWarps));
+  const long long c = blockIdx.x;
+  u0 = c < ctas ? W * c / ctas : W;
+  u1 = c < ctas ? W * (c + 1) / ctas : W;
+  if (u0 >= u1) {
+    if (tid == 0) p.rec[c] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  if (!p.sel) {  // the sequence that holds unit u0
+    long long before = 0;
+    for (int i0 = 0; i0 < p.s.B; i0 += kSplitThreads) {
+      const int i = i0 + tid;
+      long long w = 0;
+      if (i < p.s.B) {
+        int tiles, units, t0, T, pos0;
+        seq_work<MT>(p, i, tiles, units, t0, T, pos0);
+        w = (long long)tiles * units * p.c.Hk;
+      }
+      const long long incl = warp_incl_scan64(w);
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      long long base = before;
+      for (int k = 0; k < kSplitWarps; ++k) {
+        if (k < warp) base += s_sum[k];
+        before += s_sum[k];
+      }
+      const long long lo = base + incl - w;
+      if (w > 0 && lo <= u0 && u0 < lo + w) {
+        s_b = i;
+        s_pre = lo;
+      }
+      if (before > u0) break;  // uniform
+    }
+    __syncthreads();
+    b = s_b;
+    pre = s_pre;
+  }
+
+  int n_issued = 0;  // units issued by this warp so far: stage and phase
+  int4 rec = make_int4(-1, 0, 0, 0);
+  for (long long u = u0; u < u1;) {
+    // ---- the tile that holds unit u ----
+    Tile tl;
+    long long tile_begin;
+    int64_t list_at = 0;
+    if (p.sel) {
+      const long long idx = u / list_units;
+      tile_begin = idx * list_units;
+      const int x = (int)(idx % xt);
+      const long long th = idx / xt;
+      const int64_t tok = th / p.c.Hk;
+      tl.h = (int)(th - tok * p.c.Hk);
+      tl.b = max(seq_of(p.s, tok), 0);
+      tl.tok0 = (int)tok;
+      tl.pos0 = (int)max((int64_t)-0x40000000,
+                         (int64_t)p.s.lens[tl.b] - p.s.cu[tl.b + 1] + tok);
+      tl.row0 = x * S::ROWS;
+      tl.nrows = min(S::ROWS, p.G - tl.row0);
+      tl.units = list_units;
+      list_at = (tok * p.c.Hk + tl.h) * p.n_sel;
+    } else {
+      int tiles, units, t0, T, pos0;
+      seq_work<MT>(p, b, tiles, units, t0, T, pos0);
+      while (u - pre >= (long long)tiles * units * p.c.Hk) {
+        pre += (long long)tiles * units * p.c.Hk;
+        ++b;
+        seq_work<MT>(p, b, tiles, units, t0, T, pos0);
+      }
+      const long long idx = (u - pre) / units;
+      tile_begin = pre + idx * units;
+      const int x = (int)(idx / p.c.Hk);
+      tl.b = b;
+      tl.h = (int)(idx - (long long)x * p.c.Hk);
+      tl.row0 = x * S::ROWS;
+      tl.nrows = min(S::ROWS, T * p.G - tl.row0);
+      tl.tok0 = t0;
+      tl.pos0 = pos0;
+      tl.units = units;
+    }
+    tl.pos_first = tl.pos0 + tl.row0 / p.G;
+    tl.pos_last = tl.pos0 + (tl.row0 + tl.nrows - 1) / p.G;
+    const int first = (int)(u - tile_begin);
+    const int last = (int)min(u1 - tile_begin, (long long)tl.units);  // units [first, last)
+
+    // ---- query rows: power-of-two scaled fp16 fragments ----
+    uint32_t qa[MT][KS][4];
+    float fac[MT][2];
+    int row_pos[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // rows g, g + 8
+        const int r = mt * 16 + half * 8 + g;
+        const int R = tl.row0 + min(r, tl.nrows - 1);
+        const int tok = R / p.G;
+        row_pos[mt][half] = min(tl.pos0 + tok, kNoPos - 1);
+        const uint16_t *src = p.q + (int64_t)(tl.tok0 + tok) * p.q_stride +
+                              (int64_t)(tl.h * p.G + R - tok * p.G) * D;
+        uint32_t w[KS * 2];
+        float big = 0.f;
+#pragma unroll
+        for (int hh = 0; hh < D / 64; ++hh) {
+          const uint4 a = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t);
+          const uint4 bq = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t + 8);
+          const uint32_t ws[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[hh * 8 + e] = ws[e];
+            big = fmaxf(big, fabsf(__uint_as_float(ws[e] << 16)));
+            big = fmaxf(big, fabsf(__uint_as_float(ws[e] & 0xffff0000u)));
+          }
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^-e with 2^e <= big < 2^(e+1), kept normal; 1 for zero or infinity
+        const uint32_t eb = __float_as_uint(big) >> 23;
+        const uint32_t sb = (big > 0.f && eb < 255u) ? max(254u - eb, 1u) : 127u;
+        const uint32_t sbits = min(sb, 253u) << 23;
+        const float down = __uint_as_float(sbits);
+        const float up = __uint_as_float((254u - (sbits >> 23)) << 23);
+        fac[mt][half] = p.sm_scale * 1.44269504088896340736f * up;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = w[s * 2 + e];
+            qa[mt][s][half + 2 * e] =
+                pack_f16(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+          }
+        }
+      }
+
+    // ---- state ----
+    float o[MT][NT][4], m[MT][2], z[MT][2], l[MT][2];  // weights are 2^(x - z)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      z[mt][0] = z[mt][1] = 0.f;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+
+    // ---- this warp's units: first + warp, + kSplitWarps, ... ----
+    const int mine = last - first > warp ? (last - first - warp + kSplitWarps - 1) / kSplitWarps : 0;
+    // What a lane knows of unit 32 k + lane of this warp: the row of its keys
+    // in the cache (-1: nothing to do), its first position and its scales.
+    // With 16-token pages a unit is two pages.
+    struct Meta {
+      int row[P16 ? 2 : 1], pos[P16 ? 2 : 1];
+      float ks[P16 ? 2 : 1], vs[P16 ? 2 : 1];
+    } cur, nxt;
+    auto load_meta = [&](Meta &M, int k) {
+      const int i = k * 32 + lane;  // of this warp
+      const int un = first + warp + i * kSplitWarps;
+#pragma unroll
+      for (int e = 0; e < (P16 ? 2 : 1); ++e) {
+        M.row[e] = -1;
+        M.pos[e] = kNoPos;
+        M.ks[e] = M.vs[e] = 0.f;
+        if (i >= mine) continue;
+        int j, sub = 0;
+        if (p.sel) {
+          const int at = P16 ? 2 * un + e : un >> (p.c.bs_shift - 5);
+          if (!P16) sub = un & ((p.c.bs >> 5) - 1);
+          j = at < p.n_sel ? p.sel[list_at + at] : -1;
+        } else {
+          j = P16 ? 2 * un + e : un >> (p.c.bs_shift - 5);
+          if (!P16) sub = un & ((p.c.bs >> 5) - 1);
+        }
+        if (j < 0 || (int64_t)j << p.c.bs_shift > tl.pos_last) continue;
+        const int pos = (j << p.c.bs_shift) + sub * kUnit;
+        if (pos > tl.pos_last) continue;
+        const int page = j < p.s.width ? p.s.table[(int64_t)tl.b * p.s.width + j] : -1;
+        if (page < 0 || page >= p.c.pages) {
+          raise_status(kStatusBadIndex);
+          continue;
+        }
+        const int ph = page * p.c.Hk + tl.h;
+        M.row[e] = (ph << p.c.bs_shift) + sub * kUnit;
+        M.pos[e] = pos;
+        M.ks[e] = p.c.k_scale[ph];
+        M.vs[e] = p.c.v_scale[ph];
+      }
+    };
+    load_meta(cur, 0);
+    load_meta(nxt, 1);
+    int group = 0;      // cur holds units 32 group .. of this warp
+    const int base = n_issued;
+    auto issue = [&](int i) {  // unit i of this warp into its stage
+      int row[P16 ? 2 : 1];
+#pragma unroll
+      for (int e = 0; e < (P16 ? 2 : 1); ++e) {
+        const int rc = __shfl_sync(0xffffffffu, cur.row[e], i & 31);
+        const int rn = __shfl_sync(0xffffffffu, nxt.row[e], i & 31);
+        row[e] = (i >> 5) == group ? rc : rn;
+      }
+      if (lane == 0) {
+        const int st = (base + i) % kStages;
+        unsigned char *kt = ring + st * 2 * S::TILE, *vt = kt + S::TILE;
+        uint64_t *bar = &s_bar[warp][st];
+        if (!P16) {
+          mbar_arrive_expect_tx(bar, row[0] >= 0 ? 2 * S::TILE : 0);
+          if (row[0] >= 0) {
+            tma_load_rows(kt, &kmap, row[0], bar);
+            tma_load_rows(vt, &vmap, row[0], bar);
+          }
+        } else {
+          mbar_arrive_expect_tx(bar, ((row[0] >= 0) + (row[P16 ? 1 : 0] >= 0)) * S::TILE);
+#pragma unroll
+          for (int e = 0; e < (P16 ? 2 : 1); ++e)
+            if (row[e] >= 0) {
+              tma_load_rows(kt + e * (S::TILE / 2), &kmap, row[e], bar);
+              tma_load_rows(vt + e * (S::TILE / 2), &vmap, row[e], bar);
+            }
+        }
+      }
+    };
+    for (int i = 0; i < min(mine, kStages); ++i) issue(i);
+
+    for (int i = 0; i < mine; ++i) {
+      if ((i >> 5) != group) {
+        cur = nxt;
+        ++group;
+        load_meta(nxt, group + 1);
+      }
+      const int st = (base + i) % kStages;
+      mbar_wait_bounded(&s_bar[warp][st], (uint32_t)((base + i) / kStages) & 1u);
+      float ks[2], vs[2];
+      int pos[2];
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int ee = P16 ? e : 0;
+        any |= __shfl_sync(0xffffffffu, cur.row[ee], i & 31) >= 0;
+        ks[e] = __shfl_sync(0xffffffffu, cur.ks[ee], i & 31);
+        vs[e] = __shfl_sync(0xffffffffu, cur.vs[ee], i & 31);
+        pos[e] = __shfl_sync(0xffffffffu, cur.pos[ee], i & 31);
+        if (!P16 && e == 1) pos[e] += 16;
+      }
+      if (any) {
+        const unsigned char *kt = ring + st * 2 * S::TILE, *vt = kt + S::TILE;
+        // ---- S = Q K^T ----
+        float sc[MT][4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int r = n * 8 + g;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+#pragma unroll
+          for (int hh = 0; hh < D / 64; ++hh) {
+            const int chunk = D == 128 ? ((t + 4 * hh) ^ g) : (t ^ ((r >> 1) & 3));
+            const uint4 kw = *reinterpret_cast<const uint4 *>(kt + r * D + chunk * 16);
+            const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t u8 = ws[w] ^ 0x80808080u;
+              const uint32_t b0 = codes_f16<false>(u8), b1 = codes_f16<true>(u8);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][n], qa[mt][hh * 4 + w], b0, b1);
+            }
+          }
+        }
+        // ---- softmax ----
+        uint32_t pa[MT][2][4];
+        float corr[MT][2];
+        bool moved = false;
+        // a unit that ends before every row's position needs no mask
+        const bool edge = max(pos[0], pos[1]) + 15 > tl.pos_first;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float mx = m[mt][half];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = sc[mt][n][half * 2 + e] * (fac[mt][half] * ks[n >> 1]);
+                const int at = pos[n >> 1] + (n & 1) * 8 + 2 * t + e;
+                if (edge && at > row_pos[mt][half]) x = -INFINITY;
+                sc[mt][n][half * 2 + e] = x;
+                mx = fmaxf(mx, x);
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float zero = (mx == -INFINITY ? 0.f : mx) - kPBias;
+            const float old = m[mt][half];
+            corr[mt][half] = old == mx ? 1.f : old == -INFINITY ? 0.f : ex2(z[mt][half] - zero);
+            moved |= old != mx;
+            m[mt][half] = mx;
+            z[mt][half] = zero;
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float p0 = ex2(sc[mt][n][half * 2] - zero);
+              const float p1 = ex2(sc[mt][n][half * 2 + 1] - zero);
+              sum += p0 + p1;
+              pa[mt][n >> 1][(n & 1) * 2 + half] = pack_f16(p0, p1);
+            }
+            l[mt][half] = l[mt][half] * corr[mt][half] + sum;
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              o[mt][j][0] *= corr[mt][0];
+              o[mt][j][1] *= corr[mt][0];
+              o[mt][j][2] *= corr[mt][1];
+              o[mt][j][3] *= corr[mt][1];
+            }
+        }
+        // ---- O += vs * P V: column n of n-tile j is dim n * (D / 8) + j, so
+        // a thread's bytes of a token are consecutive ----
+        uint32_t vw[2][4][NT / 4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = s * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
+            if (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(vt + r * D + ((g ^ (r & 7)) * 16));
+              vw[s][k][0] = x.x ^ 0x80808080u;
+              vw[s][k][1] = x.y ^ 0x80808080u;
+              vw[s][k][NT / 4 - 2] = x.z ^ 0x80808080u;
+              vw[s][k][NT / 4 - 1] = x.w ^ 0x80808080u;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2 *>(
+                  vt + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16) + (g & 1) * 8);
+              vw[s][k][0] = x.x ^ 0x80808080u;
+              vw[s][k][1] = x.y ^ 0x80808080u;
+            }
+          }
+#pragma unroll
+        for (int w = 0; w < NT / 4; ++w) {
+          float part[MT][4][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) part[mt][j][e] = 0.f;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t a01 = __byte_perm(vw[s][0][w], vw[s][1][w], 0x5140);
+            const uint32_t a23 = __byte_perm(vw[s][0][w], vw[s][1][w], 0x7362);
+            const uint32_t b01 = __byte_perm(vw[s][2][w], vw[s][3][w], 0x5140);
+            const uint32_t b23 = __byte_perm(vw[s][2][w], vw[s][3][w], 0x7362);
+            const uint32_t f0[4] = {codes_f16<false>(a01), codes_f16<true>(a01),
+                                    codes_f16<false>(a23), codes_f16<true>(a23)};
+            const uint32_t f1[4] = {codes_f16<false>(b01), codes_f16<true>(b01),
+                                    codes_f16<false>(b23), codes_f16<true>(b23)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma_f16(part[mt][j], pa[mt][s], f0[j], f1[j]);
+            if (P16 || s == 1) {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    o[mt][w * 4 + j][e] = fmaf(vs[s], part[mt][j][e], o[mt][w * 4 + j][e]);
+                    if (P16) part[mt][j][e] = 0.f;
+                  }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (i + kStages < mine) issue(i + kStages);
+    }
+    n_issued = base + mine;
+
+    // ---- the warps' results into their rings, then merged ----
+    float *res = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float sum = l[mt][half];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = mt * 16 + half * 8 + g;
+        if (t == 0) {
+          s_m[warp][r] = sum == 0.f ? -INFINITY : z[mt][half];
+          s_l[warp][r] = sum;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < NT; j += 4)
+            *reinterpret_cast<float4 *>(res + r * S::LDO + (2 * t + e) * NT + j) =
+                make_float4(o[mt][j][half * 2 + e], o[mt][j + 1][half * 2 + e],
+                            o[mt][j + 2][half * 2 + e], o[mt][j + 3][half * 2 + e]);
+      }
+    __syncthreads();
+    const bool whole = first == 0 && last == tl.units;
+    const int slot = first > 0 ? 0 : 1;  // the end of a tile, or its beginning
+    float *part = p.part + (2 * c + slot) * S::PART;
+    for (int item = tid; item < tl.nrows * (D / 4); item += kSplitThreads) {
+      const int r = item / (D / 4), d = (item % (D / 4)) * 4;
+      float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+      const float zero = mx == -INFINITY ? 0.f : mx;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) {
+        const float f = ex2(s_m[w][r] - zero);
+        const float4 x = *reinterpret_cast<const float4 *>(
+            reinterpret_cast<float *>(ring0 + w * S::RING) + r * S::LDO + d);
+        sum = fmaf(s_l[w][r], f, sum);
+        acc.x = fmaf(x.x, f, acc.x);
+        acc.y = fmaf(x.y, f, acc.y);
+        acc.z = fmaf(x.z, f, acc.z);
+        acc.w = fmaf(x.w, f, acc.w);
+      }
+      if (whole) {
+        const int R = tl.row0 + r, tok = R / p.G;
+        const int64_t at = (int64_t)(tl.tok0 + tok) * (p.G * p.c.Hk) + tl.h * p.G + R - tok * p.G;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint2 w2;
+        w2.x = (uint32_t)__bfloat16_as_ushort(__float2bfloat16(acc.x * inv)) |
+               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16(acc.y * inv)) << 16);
+        w2.y = (uint32_t)__bfloat16_as_ushort(__float2bfloat16(acc.z * inv)) |
+               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16(acc.w * inv)) << 16);
+        *reinterpret_cast<uint2 *>(p.out + at * D + d) = w2;
+        if (d == 0 && p.lse)
+          p.lse[at] = sum == 0.f ? -INFINITY
+                                 : fmaf(zero, 0.693147180559945309417f, logf(sum));
+      } else {
+        *reinterpret_cast<float4 *>(part + r * D + d) = acc;
+        if (d == 0) {
+          part[S::ROWS * D + r] = mx;
+          part[S::ROWS * D + S::ROWS + r] = sum;
+        }
+      }
+    }
+    if (!whole) {
+      if (first > 0) {
+        rec.z = last == tl.units;          // this CTA ends a tile begun earlier
+      } else {                             // it begins one that later CTAs end
+        const int R = tl.row0;
+        rec.x = tl.tok0;
+        rec.y = tl.h | (tl.nrows << 8);
+        rec.w = R;
+      }
+    }
+    fence_proxy_async_smem();  // the rings are written by TMA again
+    __syncthreads();
+    u = tile_begin + last;
+  }
+  if (tid == 0) p.rec[c] = rec;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles that several CTAs of kv8_split_kernel shared: block (c, y) merges
+// rows 4 y .. 4 y + 3 of the tile that CTA c begins and later CTAs end, in
+// CTA order.  Two warps per row, eight partials in flight each.
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 256;
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int ctas) {
+  using S = SplitShape<D, MT>;
+  constexpr int E = D / 32;
+  __shared__ float s_o[8][D], s_ml[8][2];
+  const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait_primary();
+  const int4 rec = p.rec[c];
+  const int nrows = rec.y >> 8;
+  if (rec.x < 0 || (int)blockIdx.y * 4 >= nrows) return;
+  // the tile's partials: (c, 1), (c + 1, 0), ..., up to the CTA that ends it
+  int end = c + 1;
+  for (; end < ctas; end += 32) {
+    const bool ends = end + lane < ctas && p.rec[end + lane].z;
+    const uint32_t who = __ballot_sync(0xffffffffu, ends);
+    if (who) {
+      end += __ffs(who) - 1;
+      break;
     }
   }
-  for (int e = 0; e < E; ++e) {
-    const float y = l == 0.f ? 0.f : o[e] / l;
-    p.out[(i * H + head) * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16(y));
+  const int count = min(end, ctas - 1) - c + 1;
+  const int r = blockIdx.y * 4 + (warp >> 1);
+  const int half = (count + 1) / 2;
+  const int k0 = (warp & 1) * half, k1 = min(count, k0 + half);
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (r < nrows) {
+    auto at = [&](int k) { return p.part + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * S::PART; };
+    for (int k = k0 + lane; k < k1; k += 32) m = fmaxf(m, at(k)[S::ROWS * D + r]);
+    m = warp_max(m);
+    const float zero = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+    for (int k = k0; k < k1; ++k) {
+      const float *src = at(k);
+      const float f = ex2(src[S::ROWS * D + r] - zero);
+      l = fmaf(src[S::ROWS * D + S::ROWS + r], f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(src[r * D + lane * E + e], f, o[e]);
+    }
   }
-  if (lane == 0 && p.lse) p.lse[i * H + head] = l == 0.f ? -INFINITY : m + logf(l);
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    s_ml[warp][0] = m;
+    s_ml[warp][1] = l;
+  }
+  __syncthreads();
+  if ((warp & 1) || r >= nrows) return;
+  const float m1 = s_ml[warp + 1][0], mx = fmaxf(m, m1), zero = mx == -INFINITY ? 0.f : mx;
+  const float f0 = ex2(m - zero), f1 = ex2(m1 - zero);
+  const float sum = l * f0 + s_ml[warp + 1][1] * f1;
+  const int R = rec.w + r, tok = R / p.G;
+  const int64_t row = (int64_t)(rec.x + tok) * (p.G * p.c.Hk) + (rec.y & 255) * p.G + R - tok * p.G;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float y = (o[e] * f0 + s_o[warp + 1][lane * E + e] * f1) * inv;
+    p.out[row * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16(y));
+  }
+  if (lane == 0 && p.lse)
+    p.lse[row] =
+        sum == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(sum));
 }
 
 }  // namespace kv8

@@ -113,15 +113,17 @@ def select(q, c, table, cu, lens, n_sel, n_first, n_last, out):
 def attn(q, c, table, cu, lens, sel=None, sm_scale=None):
     """float64 -> (out [n, H, D], lse [n, H], bound on |out| error's weights).
 
-    The third result is (A, S, N) per row: the mean of |value| under the
-    softmax per dim, the largest sum of |q_d k_d| * scale over the keys, and
-    the number of keys -- what an error bound needs.  Padding rows are NaN."""
+    The third result is (A, S, N, M) per row: the mean of |value| under the
+    softmax per dim, the largest sum of |q_d k_d| * scale over the keys, the
+    number of keys and the largest |value| per dim -- what an error bound
+    needs.  Padding rows are NaN."""
     P, Hk, bs, D = c["k"].shape
     n, H = q.shape[:2]
     G = H // Hk
     sm_scale = 1 / math.sqrt(D) if sm_scale is None else sm_scale
     out, lse = np.full((n, H, D), np.nan), np.full((n, H), np.nan)
     A, S, N = np.zeros((n, H, D)), np.zeros((n, H)), np.zeros((n, H))
+    M = np.zeros((n, H, D))
     for i, b, pos in positions(cu, lens, n):
         if b < 0:
             continue
@@ -150,7 +152,8 @@ def attn(q, c, table, cu, lens, sel=None, sm_scale=None):
                 A[i, a] = p @ np.abs(v) / p.sum()
                 S[i, a] = (np.abs(k) @ np.abs(q[i, a].astype(np.float64))).max() * abs(sm_scale)
                 N[i, a] = len(k)
-    return out, lse, (A, S, N)
+                M[i, a] = np.abs(v).max(0)
+    return out, lse, (A, S, N, M)
 
 
 def attn_bounds(out, lse, info):
@@ -160,13 +163,17 @@ def attn_bounds(out, lse, info):
     taken through exp2: |error| <= delta = (D + 8) 2^-24 S (any order of the
     sum, S the sum of magnitudes).  Weights are then off by a factor within
     1 +- (2 delta + 2^-20) and rounded once to fp16 (half a step, 2^-11); sums
-    of N terms in fp32 add N 2^-24.  out is rounded once to bf16 (2^-8 of its
-    value); lse once to fp32."""
-    A, S, N = info
+    of N terms in fp32 add N 2^-24.  The largest weight of a row is held as
+    2^14, so below 2^-28 of it a weight is an fp16 subnormal, whose half step
+    is 2^-25 / 2^14 = 2^-39 of the largest weight; the sum of weights is at
+    least the largest one, so the N weights of a row add at most N 2^-39 M.
+    out is rounded once to bf16 (2^-8 of its value); lse once to fp32."""
+    A, S, N, M = info
     D = out.shape[-1]
     delta = (D + 8) * 2.0 ** -24 * S
     rel = 2 * delta + 2.0 ** -20 + 2 * N * 2.0 ** -24
-    tol_out = 2.0 ** -8 * np.abs(out) + (2.0 ** -11 + rel)[..., None] * A + 1e-30
+    tol_out = 2.0 ** -8 * np.abs(out) + (2.0 ** -11 + rel)[..., None] * A
+    tol_out += N[..., None] * 2.0 ** -39 * M + 1e-30
     with np.errstate(invalid="ignore"):
         tol_lse = rel + 2.0 ** -22 * np.where(np.isfinite(lse), np.abs(lse), 0) + 2.0 ** -24
     return tol_out, tol_lse
