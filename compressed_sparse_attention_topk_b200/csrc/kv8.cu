@@ -84,33 +84,32 @@ csa2_status launch_append_d(const kv8::AppendParams &p, cudaStream_t st) {
 
 // Kernels of an attention call and their workspace.
 struct AttnPlan {
-  int MT;          // 16-row tiles of a CTA's query rows
+  int R8;          // groups of 8 query rows in a tile
   int ctas;
   size_t part_at;  // the partials, behind one record per CTA
   size_t bytes;
 };
 
-// 16 query rows per tile, or 32 where a sequence (or, with lists, a token)
-// has more on average: a second 16-row tile reads the same fragments of the
-// cache.
+// As many query rows in a tile as a sequence (or, with lists, a token) has on
+// average, up to 32: every row of a tile reads the same fragments of the cache.
 AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
   AttnPlan a{};
   const int64_t rows = n_sel > 0 ? G : ceil_div(n * G, std::max(B, 1));
-  a.MT = rows > 16 ? 2 : 1;
-  a.ctas = 2 * device_sms();
+  a.R8 = (int)std::max<int64_t>(1, std::min<int64_t>(4, ceil_div(rows, 8)));
+  a.ctas = (a.R8 == 1 ? 3 : 2) * device_sms();
   a.part_at = align_up(size_t(a.ctas) * sizeof(int4), 256);
-  a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * 16 * a.MT * (D + 2) * 4, 256);
+  a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * 8 * a.R8 * (D + 2) * 4, 256);
   return a;
 }
 
-template <int D, int MT, bool P16>
+template <int D, int R8, bool P16>
 csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
-  using S = kv8::SplitShape<D, MT>;
+  using S = kv8::SplitShape<D, R8>;
   static std::atomic<bool> done[256];  // per device: attributes set
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 256 || !done[dev].load(std::memory_order_acquire)) {
-    if (set_smem_attr(kv8::kv8_split_kernel<D, MT, P16>, S::SMEM, false) != CSA2_OK)
+    if (set_smem_attr(kv8::kv8_split_kernel<D, R8, P16>, S::SMEM, false) != CSA2_OK)
       return CSA2_ERR_CUDA;
     if (dev >= 0 && dev < 256) done[dev].store(true, std::memory_order_release);
   }
@@ -122,7 +121,7 @@ csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
     return CSA2_ERR_CUDA;
   {
     TraceScope ts("kv8_attn_split", st);
-    kv8::kv8_split_kernel<D, MT, P16>
+    kv8::kv8_split_kernel<D, R8, P16>
         <<<(unsigned)a.ctas, kv8::kSplitThreads, S::SMEM, st>>>(km, vm, p);
     const csa2_status rc = after_launch();
     if (rc != CSA2_OK) return rc;
@@ -137,20 +136,25 @@ csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv8::kv8_merge_kernel<D, MT>, p, a.ctas) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, kv8::kv8_merge_kernel<D, R8>, p, a.ctas) != cudaSuccess)
     return CSA2_ERR_CUDA;
   return after_launch();
 }
 
-template <int D>
+template <int D, bool P16>
 csa2_status launch_attn_d(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
-  if (p.c.bs == 16)
-    return a.MT == 1 ? launch_split<D, 1, true>(p, a, st) : launch_split<D, 2, true>(p, a, st);
-  return a.MT == 1 ? launch_split<D, 1, false>(p, a, st) : launch_split<D, 2, false>(p, a, st);
+  switch (a.R8) {
+    case 1: return launch_split<D, 1, P16>(p, a, st);
+    case 2: return launch_split<D, 2, P16>(p, a, st);
+    case 3: return launch_split<D, 3, P16>(p, a, st);
+    default: return launch_split<D, 4, P16>(p, a, st);
+  }
 }
 
 csa2_status launch_attn(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
-  return p.c.D == 64 ? launch_attn_d<64>(p, a, st) : launch_attn_d<128>(p, a, st);
+  if (p.c.bs == 16)
+    return p.c.D == 64 ? launch_attn_d<64, true>(p, a, st) : launch_attn_d<128, true>(p, a, st);
+  return p.c.D == 64 ? launch_attn_d<64, false>(p, a, st) : launch_attn_d<128, false>(p, a, st);
 }
 
 }  // namespace

@@ -60,14 +60,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Bytes 0, 1 (hi = false) or 2, 3 of a word of codes with their sign bits
-// flipped (code + 128) -> two fp16 codes: 1024 + u by a byte permute, less 1152.
-template <bool HI>
+// A word whose bytes 0 and 2 are codes -> two fp16 codes: one logic operation
+// makes 1024 + (code + 128) of each, less 1152.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-  const uint32_t u = __byte_perm(w, 0x64646464u, HI ? 0x4342 : 0x4140);
+  const uint32_t u = (w & 0x00ff00ffu) ^ 0x64806480u;
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
   const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), bias);
   return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// 8 x 8 transpose of 16-bit elements over the warp (row lane / 4, columns
+// 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -79,31 +86,34 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // Few query rows per sequence (decode, drafts) or a list of blocks per token:
 // the work is the stream of the cache's bytes.
 //
-// A tile is 16 MT query rows (token-major, the group's heads inside) of one
+// A tile is 8 R8 query rows (token-major, the group's heads inside) of one
 // sequence and kv head; its keys are cut into units of 32 positions.  The
 // units of all tiles form one line, cut evenly over the CTAs (lengths differ
 // by orders of magnitude between sequences), so a CTA works on the end of a
 // tile, whole tiles and the beginning of one; a tile that several CTAs share
-// leaves a partial (m, l, O) per CTA, merged in order by kv8_merge_kernel.
+// leaves a partial (z, l, O) per CTA, merged in order by kv8_merge_kernel.
 // Within a CTA the warps take a tile's units in turn, each with its own ring
 // of units (TMA, one lane), its own softmax state and no barrier until the
-// tile's end: the 8-bit codes become fp16 fragments in registers (byte
-// permutes), and the products are mma.sync m16n8k16 -- with 16 or 32 rows
-// the tensor work is a fraction of the time the bytes take, and a 128-row
-// tcgen05 tile would be mostly padding.
+// tile's end: the 8-bit codes become fp16 fragments in registers, and the
+// products are mma.sync m16n8k16 with the cache as the 16-row operand and the
+// query rows as the 8 columns, S^T = K Q^T and O^T = V^T P^T (so 4 or 8 query
+// heads do not pay for 16, and P^T is an 8 x 8 transpose of S^T).  The tensor
+// work is a fraction of the time the bytes take; a 128-row tcgen05 tile would
+// be mostly padding.
 // ---------------------------------------------------------------------------
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kUnit = 32;
-constexpr int kStages = 3;
 constexpr int kNoPos = 1 << 30;  // a table reaches fewer positions; no row sees this one
 constexpr float kPBias = 14.f;  // weights are held as 2^14 p
 
-template <int D, int MT>
+template <int D, int R8>
 struct SplitShape {
-  static constexpr int ROWS = 16 * MT;
+  static constexpr int ROWS = 8 * R8;
+  static constexpr int CTAS = R8 == 1 ? 3 : 2;            // per SM
+  static constexpr int STAGES = (R8 == 1 ? 2 : 3) * (128 / D);
   static constexpr int TILE = kUnit * D;                  // bytes of a unit's keys (or values)
-  static constexpr int RING = kStages * 2 * TILE;         // per warp
+  static constexpr int RING = STAGES * 2 * TILE;          // per warp
   static constexpr int LDO = D + 4;                       // floats per row of a warp's result
   static constexpr size_t SMEM = size_t(kSplitWarps) * RING + 1024;
   static constexpr size_t PART = size_t(ROWS) * (D + 2);  // floats of one partial
@@ -120,7 +130,7 @@ struct Tile {
 };
 
 // Work of sequence b: tiles per kv head and units per tile.
-template <int MT>
+template <int ROWS>
 __device__ __forceinline__ void seq_work(const AttnParams &p, int b, int &tiles, int &units,
                                          int &t0, int &T, int &pos0) {
   const int32_t lo = max(p.s.cu[b], 0), hi = p.s.cu[b + 1];
@@ -128,22 +138,22 @@ __device__ __forceinline__ void seq_work(const AttnParams &p, int b, int &tiles,
   T = (int)max((int64_t)0, min64(hi, p.s.n) - lo);
   const int64_t len = p.s.lens[b];
   pos0 = (int)max((int64_t)-0x40000000, len - hi + lo);
-  tiles = (int)(((int64_t)T * p.G + 16 * MT - 1) / (16 * MT));
+  tiles = (int)(((int64_t)T * p.G + ROWS - 1) / ROWS);
   const int64_t reach = (int64_t)p.s.width << p.c.bs_shift;
   const int64_t seen = min64(max(len, (int64_t)0), reach);
   units = max(1, (int)((seen + kUnit - 1) / kUnit));
 }
 
-template <int D, int MT, bool P16>
-__global__ void __launch_bounds__(kSplitThreads, 2)
+template <int D, int R8, bool P16>
+__global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
     kv8_split_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
-  using S = SplitShape<D, MT>;
-  constexpr int NT = D / 8;    // output columns' n-tiles
-  constexpr int KS = D / 16;   // k-steps of a dot
+  using S = SplitShape<D, R8>;
+  constexpr int DT = D / 16;   // k-steps of a dot; 16-dim tiles of the output
+  constexpr int kStages = S::STAGES;
   extern __shared__ unsigned char split_smem[];
   __shared__ uint64_t s_bar[kSplitWarps][kStages];
-  __shared__ float s_m[kSplitWarps][S::ROWS], s_l[kSplitWarps][S::ROWS];
+  __shared__ float s_z[kSplitWarps][S::ROWS], s_l[kSplitWarps][S::ROWS];
   __shared__ long long s_sum[kSplitWarps];
   __shared__ long long s_pre;
   __shared__ int s_b;
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     long long mine = 0;
     for (int i = tid; i < p.s.B; i += kSplitThreads) {
       int tiles, units, t0, T, pos0;
-      seq_work<MT>(p, i, tiles, units, t0, T, pos0);
+      seq_work<S::ROWS>(p, i, tiles, units, t0, T, pos0);
       mine += (long long)tiles * units;
       if (tiles > 0 && blockIdx.x == 0 &&
           (int64_t)p.s.lens[i] > ((int64_t)p.s.width << p.c.bs_shift))
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       long long w = 0;
       if (i < p.s.B) {
         int tiles, units, t0, T, pos0;
-        seq_work<MT>(p, i, tiles, units, t0, T, pos0);
+        seq_work<S::ROWS>(p, i, tiles, units, t0, T, pos0);
         w = (long long)tiles * units * p.c.Hk;
       }
       const long long incl = warp_incl_scan64(w);
@@ -249,11 +259,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       list_at = (tok * p.c.Hk + tl.h) * p.n_sel;
     } else {
       int tiles, units, t0, T, pos0;
-      seq_work<MT>(p, b, tiles, units, t0, T, pos0);
+      seq_work<S::ROWS>(p, b, tiles, units, t0, T, pos0);
       while (u - pre >= (long long)tiles * units * p.c.Hk) {
         pre += (long long)tiles * units * p.c.Hk;
         ++b;
-        seq_work<MT>(p, b, tiles, units, t0, T, pos0);
+        seq_work<S::ROWS>(p, b, tiles, units, t0, T, pos0);
       }
       const long long idx = (u - pre) / units;
       tile_begin = pre + idx * units;
@@ -271,65 +281,65 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int first = (int)(u - tile_begin);
     const int last = (int)min(u1 - tile_begin, (long long)tl.units);  // units [first, last)
 
-    // ---- query rows: power-of-two scaled fp16 fragments ----
-    uint32_t qa[MT][KS][4];
-    float fac[MT][2];
-    int row_pos[MT][2];
+    // ---- query rows: power-of-two scaled fp16 fragments.  Thread (g, t)
+    // holds row g of each group of 8, dims 64 hh + 16 t + 4 w + (0, 2 | 1, 3)
+    // for k-step 4 hh + w, as the cache's words below ----
+    uint32_t qb[R8][DT][2];
+    float fac[R8][2];     // of rows 2 t, 2 t + 1: the columns of S^T and O^T
+    int row_pos[R8][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int q8 = 0; q8 < R8; ++q8) {
+      const int R = tl.row0 + min(q8 * 8 + g, tl.nrows - 1);
+      const int tok = R / p.G;
+      const uint16_t *src = p.q + (int64_t)(tl.tok0 + tok) * p.q_stride +
+                            (int64_t)(tl.h * p.G + R - tok * p.G) * D;
+      float big = 0.f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // rows g, g + 8
-        const int r = mt * 16 + half * 8 + g;
-        const int R = tl.row0 + min(r, tl.nrows - 1);
-        const int tok = R / p.G;
-        row_pos[mt][half] = min(tl.pos0 + tok, kNoPos - 1);
-        const uint16_t *src = p.q + (int64_t)(tl.tok0 + tok) * p.q_stride +
-                              (int64_t)(tl.h * p.G + R - tok * p.G) * D;
-        uint32_t w[KS * 2];
-        float big = 0.f;
+      for (int hh = 0; hh < D / 64; ++hh) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t);
+        const uint4 c4 = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t + 8);
+        const uint32_t ws[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-        for (int hh = 0; hh < D / 64; ++hh) {
-          const uint4 a = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t);
-          const uint4 bq = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t + 8);
-          const uint32_t ws[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            w[hh * 8 + e] = ws[e];
-            big = fmaxf(big, fabsf(__uint_as_float(ws[e] << 16)));
-            big = fmaxf(big, fabsf(__uint_as_float(ws[e] & 0xffff0000u)));
-          }
-        }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // 2^-e with 2^e <= big < 2^(e+1), kept normal; 1 for zero or infinity
-        const uint32_t eb = __float_as_uint(big) >> 23;
-        const uint32_t sb = (big > 0.f && eb < 255u) ? max(254u - eb, 1u) : 127u;
-        const uint32_t sbits = min(sb, 253u) << 23;
-        const float down = __uint_as_float(sbits);
-        const float up = __uint_as_float((254u - (sbits >> 23)) << 23);
-        fac[mt][half] = p.sm_scale * 1.44269504088896340736f * up;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t x = w[s * 2 + e];
-            qa[mt][s][half + 2 * e] =
-                pack_f16(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
-          }
+        for (int e = 0; e < 8; ++e) {
+          qb[q8][hh * 4 + e / 2][e & 1] = ws[e];
+          big = fmaxf(big, fabsf(__uint_as_float(ws[e] << 16)));
+          big = fmaxf(big, fabsf(__uint_as_float(ws[e] & 0xffff0000u)));
         }
       }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // 2^-e with 2^e <= big < 2^(e+1), kept normal; 1 for zero or infinity
+      const uint32_t eb = __float_as_uint(big) >> 23;
+      const uint32_t sb =
+          min((big > 0.f && eb < 255u) ? max(254u - eb, 1u) : 127u, 253u);
+      const float down = __uint_as_float(sb << 23);
+      const float f = p.sm_scale * 1.44269504088896340736f * __uint_as_float((254u - sb) << 23);
+      const int pos = min(tl.pos0 + tok, kNoPos - 1);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fac[q8][e] = __shfl_sync(0xffffffffu, f, (2 * t + e) * 4);
+        row_pos[q8][e] = __shfl_sync(0xffffffffu, pos, (2 * t + e) * 4);
+      }
+#pragma unroll
+      for (int s = 0; s < DT; ++s) {
+        const uint32_t w0 = qb[q8][s][0], w1 = qb[q8][s][1];  // dims 0, 1 and 2, 3
+        qb[q8][s][0] = pack_f16(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down);
+        qb[q8][s][1] = pack_f16(__uint_as_float(w0 & 0xffff0000u) * down,
+                                __uint_as_float(w1 & 0xffff0000u) * down);
+      }
+    }
 
-    // ---- state ----
-    float o[MT][NT][4], m[MT][2], z[MT][2], l[MT][2];  // weights are 2^(x - z)
+    // ---- state: weights are 2^(x - z) ----
+    float o[R8][DT][4], m[R8][2], z[R8][2], l[R8][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int q8 = 0; q8 < R8; ++q8) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < DT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      z[mt][0] = z[mt][1] = 0.f;
-      l[mt][0] = l[mt][1] = 0.f;
+        for (int e = 0; e < 4; ++e) o[q8][j][e] = 0.f;
+      m[q8][0] = m[q8][1] = -INFINITY;
+      z[q8][0] = z[q8][1] = 0.f;
+      l[q8][0] = l[q8][1] = 0.f;
     }
 
     // ---- this warp's units: first + warp, + kSplitWarps, ... ----
@@ -431,134 +441,138 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       }
       if (any) {
         const unsigned char *kt = ring + st * 2 * S::TILE, *vt = kt + S::TILE;
-        // ---- S = Q K^T ----
-        float sc[MT][4][4];
+        // ---- S^T = K Q^T: 16 positions per row tile ----
+        float sc[R8][2][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int r = n * 8 + g;
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sc[q8][k][e] = 0.f;
+          const int r = k * 16 + g;  // and r + 8: the same place in the swizzle
 #pragma unroll
           for (int hh = 0; hh < D / 64; ++hh) {
-            const int chunk = D == 128 ? ((t + 4 * hh) ^ g) : (t ^ ((r >> 1) & 3));
-            const uint4 kw = *reinterpret_cast<const uint4 *>(kt + r * D + chunk * 16);
-            const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
+            const int chunk = D == 128 ? ((t + 4 * hh) ^ g) : (t ^ ((g >> 1) & 3));
+            const uint4 x = *reinterpret_cast<const uint4 *>(kt + r * D + chunk * 16);
+            const uint4 y = *reinterpret_cast<const uint4 *>(kt + (r + 8) * D + chunk * 16);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t u8 = ws[w] ^ 0x80808080u;
-              const uint32_t b0 = codes_f16<false>(u8), b1 = codes_f16<true>(u8);
+              const uint32_t a[4] = {codes_f16(xs[w]), codes_f16(ys[w]), codes_f16(xs[w] >> 8),
+                                     codes_f16(ys[w] >> 8)};
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_f16(sc[mt][n], qa[mt][hh * 4 + w], b0, b1);
+              for (int q8 = 0; q8 < R8; ++q8)
+                mma_f16(sc[q8][k], a, qb[q8][hh * 4 + w][0], qb[q8][hh * 4 + w][1]);
             }
           }
         }
-        // ---- softmax ----
-        uint32_t pa[MT][2][4];
-        float corr[MT][2];
+        // ---- softmax: a thread has positions g, g + 8 of each 16 and rows
+        // 2 t, 2 t + 1 of each 8 ----
+#pragma unroll
+        for (int q8 = 0; q8 < R8; ++q8)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[q8][k][e] *= fac[q8][e & 1] * ks[k];
+        if (max(pos[0], pos[1]) + 15 > tl.pos_first) {  // not seen whole by every row
+#pragma unroll
+          for (int q8 = 0; q8 < R8; ++q8)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (pos[k] + g + (e >> 1) * 8 > row_pos[q8][e & 1]) sc[q8][k][e] = -INFINITY;
+        }
+        uint32_t pb[R8][2][2];
+        float corr[R8][2];
         bool moved = false;
-        // a unit that ends before every row's position needs no mask
-        const bool edge = max(pos[0], pos[1]) + 15 > tl.pos_first;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int q8 = 0; q8 < R8; ++q8) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float mx = m[mt][half];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x = sc[mt][n][half * 2 + e] * (fac[mt][half] * ks[n >> 1]);
-                const int at = pos[n >> 1] + (n & 1) * 8 + 2 * t + e;
-                if (edge && at > row_pos[mt][half]) x = -INFINITY;
-                sc[mt][n][half * 2 + e] = x;
-                mx = fmaxf(mx, x);
-              }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(sc[q8][0][e], sc[q8][0][e + 2]),
+                             fmaxf(sc[q8][1][e], sc[q8][1][e + 2]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float old = m[q8][e];
+            mx = fmaxf(mx, old);
             const float zero = (mx == -INFINITY ? 0.f : mx) - kPBias;
-            const float old = m[mt][half];
-            corr[mt][half] = old == mx ? 1.f : old == -INFINITY ? 0.f : ex2(z[mt][half] - zero);
+            corr[q8][e] = old == mx ? 1.f : old == -INFINITY ? 0.f : ex2(z[q8][e] - zero);
             moved |= old != mx;
-            m[mt][half] = mx;
-            z[mt][half] = zero;
+            m[q8][e] = mx;
+            z[q8][e] = zero;
             float sum = 0.f;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const float p0 = ex2(sc[mt][n][half * 2] - zero);
-              const float p1 = ex2(sc[mt][n][half * 2 + 1] - zero);
-              sum += p0 + p1;
-              pa[mt][n >> 1][(n & 1) * 2 + half] = pack_f16(p0, p1);
+            for (int k = 0; k < 2; ++k) {
+              sc[q8][k][e] = ex2(sc[q8][k][e] - zero);
+              sc[q8][k][e + 2] = ex2(sc[q8][k][e + 2] - zero);
+              sum += sc[q8][k][e] + sc[q8][k][e + 2];
             }
-            l[mt][half] = l[mt][half] * corr[mt][half] + sum;
+            l[q8][e] = l[q8][e] * corr[q8][e] + sum;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            pb[q8][k][0] = transpose_8x8(pack_f16(sc[q8][k][0], sc[q8][k][1]));
+            pb[q8][k][1] = transpose_8x8(pack_f16(sc[q8][k][2], sc[q8][k][3]));
           }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              o[mt][j][0] *= corr[mt][0];
-              o[mt][j][1] *= corr[mt][0];
-              o[mt][j][2] *= corr[mt][1];
-              o[mt][j][3] *= corr[mt][1];
-            }
+            for (int j = 0; j < DT; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[q8][j][e] *= corr[q8][e & 1];
         }
-        // ---- O += vs * P V: column n of n-tile j is dim n * (D / 8) + j, so
-        // a thread's bytes of a token are consecutive ----
-        uint32_t vw[2][4][NT / 4];
+        // ---- O^T += vs * V^T P^T: rows g and g + 8 of 16-dim tile j are
+        // dims g DT 2 + j and + DT + j, so a thread's bytes of a token are
+        // consecutive ----
+        uint32_t vw[2][4][D / 32];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = s * 16 + 2 * t + (k & 1) + (k >> 1) * 8;
-            if (D == 128) {
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const int r = k * 16 + 2 * t + (i4 & 1) + (i4 >> 1) * 8;
+            if constexpr (D == 128) {
               const uint4 x = *reinterpret_cast<const uint4 *>(vt + r * D + ((g ^ (r & 7)) * 16));
-              vw[s][k][0] = x.x ^ 0x80808080u;
-              vw[s][k][1] = x.y ^ 0x80808080u;
-              vw[s][k][NT / 4 - 2] = x.z ^ 0x80808080u;
-              vw[s][k][NT / 4 - 1] = x.w ^ 0x80808080u;
+              vw[k][i4][0] = x.x;
+              vw[k][i4][1] = x.y;
+              vw[k][i4][2] = x.z;
+              vw[k][i4][3] = x.w;
             } else {
               const uint2 x = *reinterpret_cast<const uint2 *>(
                   vt + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16) + (g & 1) * 8);
-              vw[s][k][0] = x.x ^ 0x80808080u;
-              vw[s][k][1] = x.y ^ 0x80808080u;
+              vw[k][i4][0] = x.x;
+              vw[k][i4][1] = x.y;
             }
           }
 #pragma unroll
-        for (int w = 0; w < NT / 4; ++w) {
-          float part[MT][4][4];
+        for (int j = 0; j < DT; ++j) {
+          // byte j % 4 of words j / 4 (dim row g) and j / 4 + D / 64 (row g + 8)
+          const int lo = j / 4, hi = lo + D / 64;
+          const uint32_t pick = (uint32_t)((4 + j % 4) << 8 | j % 4);
+          float part[R8][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int e = 0; e < 4; ++e) part[q8][e] = 0.f;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) part[mt][j][e] = 0.f;
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t a[4] = {codes_f16(__byte_perm(vw[k][0][lo], vw[k][1][lo], pick)),
+                                   codes_f16(__byte_perm(vw[k][0][hi], vw[k][1][hi], pick)),
+                                   codes_f16(__byte_perm(vw[k][2][lo], vw[k][3][lo], pick)),
+                                   codes_f16(__byte_perm(vw[k][2][hi], vw[k][3][hi], pick))};
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t a01 = __byte_perm(vw[s][0][w], vw[s][1][w], 0x5140);
-            const uint32_t a23 = __byte_perm(vw[s][0][w], vw[s][1][w], 0x7362);
-            const uint32_t b01 = __byte_perm(vw[s][2][w], vw[s][3][w], 0x5140);
-            const uint32_t b23 = __byte_perm(vw[s][2][w], vw[s][3][w], 0x7362);
-            const uint32_t f0[4] = {codes_f16<false>(a01), codes_f16<true>(a01),
-                                    codes_f16<false>(a23), codes_f16<true>(a23)};
-            const uint32_t f1[4] = {codes_f16<false>(b01), codes_f16<true>(b01),
-                                    codes_f16<false>(b23), codes_f16<true>(b23)};
+            for (int q8 = 0; q8 < R8; ++q8) mma_f16(part[q8], a, pb[q8][k][0], pb[q8][k][1]);
+            if (P16 || k == 1) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+              for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_f16(part[mt][j], pa[mt][s], f0[j], f1[j]);
-            if (P16 || s == 1) {
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    o[mt][w * 4 + j][e] = fmaf(vs[s], part[mt][j][e], o[mt][w * 4 + j][e]);
-                    if (P16) part[mt][j][e] = 0.f;
-                  }
+                for (int e = 0; e < 4; ++e) {
+                  o[q8][j][e] = fmaf(vs[k], part[q8][e], o[q8][j][e]);
+                  if (P16) part[q8][e] = 0.f;
+                }
             }
           }
         }
@@ -571,24 +585,25 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     // ---- the warps' results into their rings, then merged ----
     float *res = reinterpret_cast<float *>(ring);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float sum = l[mt][half];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = mt * 16 + half * 8 + g;
-        if (t == 0) {
-          s_m[warp][r] = sum == 0.f ? -INFINITY : z[mt][half];
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[q8][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int r = q8 * 8 + 2 * t + e;
+        if (g == 0) {
+          s_z[warp][r] = sum == 0.f ? -INFINITY : z[q8][e];
           s_l[warp][r] = sum;
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int j = 0; j < NT; j += 4)
-            *reinterpret_cast<float4 *>(res + r * S::LDO + (2 * t + e) * NT + j) =
-                make_float4(o[mt][j][half * 2 + e], o[mt][j + 1][half * 2 + e],
-                            o[mt][j + 2][half * 2 + e], o[mt][j + 3][half * 2 + e]);
+          for (int j = 0; j < DT; j += 4)
+            *reinterpret_cast<float4 *>(res + r * S::LDO + (2 * g + half) * DT + j) = make_float4(
+                o[q8][j][half * 2 + e], o[q8][j + 1][half * 2 + e], o[q8][j + 2][half * 2 + e],
+                o[q8][j + 3][half * 2 + e]);
       }
     __syncthreads();
     const bool whole = first == 0 && last == tl.units;
@@ -598,12 +613,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
       const int r = item / (D / 4), d = (item % (D / 4)) * 4;
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kSplitWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+      for (int w = 0; w < kSplitWarps; ++w) mx = fmaxf(mx, s_z[w][r]);
       const float zero = mx == -INFINITY ? 0.f : mx;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kSplitWarps; ++w) {
-        const float f = ex2(s_m[w][r] - zero);
+        const float f = ex2(s_z[w][r] - zero);
         const float4 x = *reinterpret_cast<const float4 *>(
             reinterpret_cast<float *>(ring0 + w * S::RING) + r * S::LDO + d);
         sum = fmaf(s_l[w][r], f, sum);
@@ -657,9 +672,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 
-template <int D, int MT>
+template <int D, int R8>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int ctas) {
-  using S = SplitShape<D, MT>;
+  using S = SplitShape<D, R8>;
   constexpr int E = D / 32;
   __shared__ float s_o[8][D], s_ml[8][2];
   const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
