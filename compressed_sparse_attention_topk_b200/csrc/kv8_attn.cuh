@@ -45,6 +45,19 @@ __device__ __forceinline__ void tma_load_rows(void *smem, const CUtensorMap *map
       : "memory");
 }
 
+// Bounded wait whose polls may suspend the warp, leaving its issue slots to
+// the others of the SM: ~2^32 cycles at most, then recorded (bit 1).
+__device__ __forceinline__ void mbar_wait_suspended(uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  const long long start = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - start > (1ll << 32)) {
+      raise_status(kStatusWaitTimeout);
+      return;
+    }
+  }
+}
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -54,16 +67,30 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+      "%9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// A word whose bytes 0 and 2 are codes -> two fp16 codes: one logic operation
-// makes 1024 + (code + 128) of each, less 1152.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-  const uint32_t u = (w & 0x00ff00ffu) ^ 0x64806480u;
+// A word whose bytes 0 and 2 are codes -> two fp16 codes: one three-input
+// logic operation, (w & 0x00ff00ff) ^ 0x64806480, makes 1024 + (code + 128) of
+// each, less 1152.  `flip` is that second constant in a register that the
+// compiler cannot see through: with both as immediates it takes two operations.
+constexpr uint32_t kFlip = 0x64806480u;
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t flip) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, 0x00ff00ff, %2, 0x6a;" : "=r"(u) : "r"(w), "r"(flip));
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
   const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), bias);
   return *reinterpret_cast<const uint32_t *>(&r);
@@ -167,6 +194,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
     fence_barrier_init();
   }
   pdl_allow_dependents();
+  uint32_t flip;
+  asm volatile("mov.b32 %0, %1;" : "=r"(flip) : "n"(kFlip));
 
   // ---- the line of units: its length, and this CTA's stretch of it ----
   long long W, u0, u1;
@@ -426,18 +455,21 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
         load_meta(nxt, group + 1);
       }
       const int st = (base + i) % kStages;
-      mbar_wait_bounded(&s_bar[warp][st], (uint32_t)((base + i) / kStages) & 1u);
+      mbar_wait_suspended(&s_bar[warp][st], (uint32_t)((base + i) / kStages) & 1u);
       float ks[2], vs[2];
       int pos[2];
       bool any = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int ee = P16 ? e : 0;
-        any |= __shfl_sync(0xffffffffu, cur.row[ee], i & 31) >= 0;
-        ks[e] = __shfl_sync(0xffffffffu, cur.ks[ee], i & 31);
-        vs[e] = __shfl_sync(0xffffffffu, cur.vs[ee], i & 31);
-        pos[e] = __shfl_sync(0xffffffffu, cur.pos[ee], i & 31);
-        if (!P16 && e == 1) pos[e] += 16;
+      for (int e = 0; e < (P16 ? 2 : 1); ++e) {
+        ks[e] = __shfl_sync(0xffffffffu, cur.ks[e], i & 31);
+        vs[e] = __shfl_sync(0xffffffffu, cur.vs[e], i & 31);
+        pos[e] = __shfl_sync(0xffffffffu, cur.pos[e], i & 31);
+        any |= pos[e] != kNoPos;
+      }
+      if (!P16) {
+        ks[1] = ks[0];
+        vs[1] = vs[0];
+        pos[1] = pos[0] + 16;
       }
       if (any) {
         const unsigned char *kt = ring + st * 2 * S::TILE, *vt = kt + S::TILE;
@@ -445,10 +477,6 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
         float sc[R8][2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int q8 = 0; q8 < R8; ++q8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[q8][k][e] = 0.f;
           const int r = k * 16 + g;  // and r + 8: the same place in the swizzle
 #pragma unroll
           for (int hh = 0; hh < D / 64; ++hh) {
@@ -458,11 +486,15 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t a[4] = {codes_f16(xs[w]), codes_f16(ys[w]), codes_f16(xs[w] >> 8),
-                                     codes_f16(ys[w] >> 8)};
+              const uint32_t a[4] = {codes_f16(xs[w], flip), codes_f16(ys[w], flip),
+                                     codes_f16(xs[w] >> 8, flip), codes_f16(ys[w] >> 8, flip)};
 #pragma unroll
-              for (int q8 = 0; q8 < R8; ++q8)
-                mma_f16(sc[q8][k], a, qb[q8][hh * 4 + w][0], qb[q8][hh * 4 + w][1]);
+              for (int q8 = 0; q8 < R8; ++q8) {
+                if (hh == 0 && w == 0)
+                  mma_f16_first(sc[q8][k], a, qb[q8][0][0], qb[q8][0][1]);
+                else
+                  mma_f16(sc[q8][k], a, qb[q8][hh * 4 + w][0], qb[q8][hh * 4 + w][1]);
+              }
             }
           }
         }
@@ -554,25 +586,25 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
           const uint32_t pick = (uint32_t)((4 + j % 4) << 8 | j % 4);
           float part[R8][4];
 #pragma unroll
-          for (int q8 = 0; q8 < R8; ++q8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[q8][e] = 0.f;
-#pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {codes_f16(__byte_perm(vw[k][0][lo], vw[k][1][lo], pick)),
-                                   codes_f16(__byte_perm(vw[k][0][hi], vw[k][1][hi], pick)),
-                                   codes_f16(__byte_perm(vw[k][2][lo], vw[k][3][lo], pick)),
-                                   codes_f16(__byte_perm(vw[k][2][hi], vw[k][3][hi], pick))};
+            const uint32_t a[4] = {
+                codes_f16(__byte_perm(vw[k][0][lo], vw[k][1][lo], pick), flip),
+                codes_f16(__byte_perm(vw[k][0][hi], vw[k][1][hi], pick), flip),
+                codes_f16(__byte_perm(vw[k][2][lo], vw[k][3][lo], pick), flip),
+                codes_f16(__byte_perm(vw[k][2][hi], vw[k][3][hi], pick), flip)};
 #pragma unroll
-            for (int q8 = 0; q8 < R8; ++q8) mma_f16(part[q8], a, pb[q8][k][0], pb[q8][k][1]);
+            for (int q8 = 0; q8 < R8; ++q8) {
+              if (P16 || k == 0)
+                mma_f16_first(part[q8], a, pb[q8][k][0], pb[q8][k][1]);
+              else
+                mma_f16(part[q8], a, pb[q8][k][0], pb[q8][k][1]);
+            }
             if (P16 || k == 1) {
 #pragma unroll
               for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 4; ++e)
                   o[q8][j][e] = fmaf(vs[k], part[q8][e], o[q8][j][e]);
-                  if (P16) part[q8][e] = 0.f;
-                }
             }
           }
         }
