@@ -12,6 +12,7 @@
 #include "host.cuh"
 #include "kv8_attn.cuh"
 #include "kv8_cache.cuh"
+#include "kv8_chunk.cuh"
 #include "kv8_select.cuh"
 
 namespace csa2 {
@@ -82,24 +83,66 @@ csa2_status launch_append_d(const kv8::AppendParams &p, cudaStream_t st) {
   return after_launch();
 }
 
-// Kernels of an attention call and their workspace.
+// The kernel of an attention call and its workspace.
 struct AttnPlan {
-  int R8;          // groups of 8 query rows in a tile
+  bool chunk;      // 256-row tiles on tcgen05
+  int R8;          // else: groups of 8 query rows in a tile
   int ctas;
   size_t part_at;  // the partials, behind one record per CTA
   size_t bytes;
 };
 
 // As many query rows in a tile as a sequence (or, with lists, a token) has on
-// average, up to 32: every row of a tile reads the same fragments of the cache.
+// average, up to 32: every row of a tile reads the same fragments of the
+// cache.  More rows than that go to the tensor-core tiles.
 AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
   AttnPlan a{};
   const int64_t rows = n_sel > 0 ? G : ceil_div(n * G, std::max(B, 1));
+  a.chunk = n_sel == 0 && rows > 32;
   a.R8 = (int)std::max<int64_t>(1, std::min<int64_t>(4, ceil_div(rows, 8)));
-  a.ctas = (a.R8 == 1 ? 3 : 2) * device_sms();
+  a.ctas = (a.chunk ? 1 : a.R8 == 1 ? 3 : 2) * device_sms();
   a.part_at = align_up(size_t(a.ctas) * sizeof(int4), 256);
-  a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * 8 * a.R8 * (D + 2) * 4, 256);
+  const size_t tile_rows = a.chunk ? kv8::kChunkRows : 8 * a.R8;
+  a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * tile_rows * (D + 2) * 4, 256);
   return a;
+}
+
+// Merges the tiles that several CTAs shared; its blocks come up while the
+// attention kernel's last ones run.
+template <int D, int ROWS>
+csa2_status launch_merge(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+  TraceScope ts("kv8_attn_merge", st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.ctas, ROWS / 4);
+  cfg.blockDim = dim3(kv8::kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv8::kv8_merge_kernel<D, ROWS>, p, a.ctas) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  return after_launch();
+}
+
+template <int D>
+csa2_status launch_chunk(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+  const size_t smem = kv8::chunk_smem_bytes<D>();
+  static std::atomic<bool> done[256];  // per device: attributes set
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 256 || !done[dev].load(std::memory_order_acquire)) {
+    if (set_smem_attr(kv8::kv8_chunk_kernel<D>, smem, false) != CSA2_OK) return CSA2_ERR_CUDA;
+    if (dev >= 0 && dev < 256) done[dev].store(true, std::memory_order_release);
+  }
+  {
+    TraceScope ts("kv8_attn_chunk", st);
+    kv8::kv8_chunk_kernel<D><<<(unsigned)a.ctas, kv8::kChunkThreads, smem, st>>>(p);
+    const csa2_status rc = after_launch();
+    if (rc != CSA2_OK) return rc;
+  }
+  return launch_merge<D, kv8::kChunkRows>(p, a, st);
 }
 
 template <int D, int R8, bool P16>
@@ -126,19 +169,7 @@ csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
     const csa2_status rc = after_launch();
     if (rc != CSA2_OK) return rc;
   }
-  TraceScope ts("kv8_attn_merge", st);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.ctas, S::ROWS / 4);
-  cfg.blockDim = dim3(kv8::kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv8::kv8_merge_kernel<D, R8>, p, a.ctas) != cudaSuccess)
-    return CSA2_ERR_CUDA;
-  return after_launch();
+  return launch_merge<D, S::ROWS>(p, a, st);
 }
 
 template <int D, bool P16>
@@ -152,6 +183,7 @@ csa2_status launch_attn_d(const kv8::AttnParams &p, const AttnPlan &a, cudaStrea
 }
 
 csa2_status launch_attn(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+  if (a.chunk) return p.c.D == 64 ? launch_chunk<64>(p, a, st) : launch_chunk<128>(p, a, st);
   if (p.c.bs == 16)
     return p.c.D == 64 ? launch_attn_d<64, true>(p, a, st) : launch_attn_d<128, true>(p, a, st);
   return p.c.D == 64 ? launch_attn_d<64, false>(p, a, st) : launch_attn_d<128, false>(p, a, st);

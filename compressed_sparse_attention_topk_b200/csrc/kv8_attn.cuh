@@ -698,15 +698,16 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 }
 
 // ---------------------------------------------------------------------------
-// Tiles that several CTAs of kv8_split_kernel shared: block (c, y) merges
+// Tiles of ROWS query rows that several CTAs shared (of kv8_split_kernel, or
+// of kv8_chunk_kernel): block (c, y) merges
 // rows 4 y .. 4 y + 3 of the tile that CTA c begins and later CTAs end, in
 // CTA order.  Two warps per row, eight partials in flight each.
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 
-template <int D, int R8>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int ctas) {
-  using S = SplitShape<D, R8>;
+  constexpr size_t PART = size_t(ROWS) * (D + 2);
   constexpr int E = D / 32;
   __shared__ float s_o[8][D], s_ml[8][2];
   const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -732,15 +733,15 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   if (r < nrows) {
-    auto at = [&](int k) { return p.part + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * S::PART; };
-    for (int k = k0 + lane; k < k1; k += 32) m = fmaxf(m, at(k)[S::ROWS * D + r]);
+    auto at = [&](int k) { return p.part + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * PART; };
+    for (int k = k0 + lane; k < k1; k += 32) m = fmaxf(m, at(k)[ROWS * D + r]);
     m = warp_max(m);
     const float zero = m == -INFINITY ? 0.f : m;
 #pragma unroll 8
     for (int k = k0; k < k1; ++k) {
       const float *src = at(k);
-      const float f = ex2(src[S::ROWS * D + r] - zero);
-      l = fmaf(src[S::ROWS * D + S::ROWS + r], f, l);
+      const float f = ex2(src[ROWS * D + r] - zero);
+      l = fmaf(src[ROWS * D + ROWS + r], f, l);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(src[r * D + lane * E + e], f, o[e]);
     }

@@ -1,0 +1,729 @@
+// Attention over the 8-bit paged cache for many query rows per sequence (a
+// prompt or a chunk of one): the mathematics of kv8_attn.cuh on the
+// 5th-generation tensor cores.
+//
+// A CTA holds 256 query rows (token-major, the group's heads inside) of one
+// sequence and kv head as two 128-row tiles, and passes over its keys 128 at
+// a time.  Per step and tile: S = Q K^T (tcgen05, fp16 x fp16 -> fp32 in
+// TMEM), one thread per row takes the softmax and leaves the weights in TMEM
+// over S, O += P V (the weights as the TMEM operand).  Eight further warps
+// turn the next step's codes into fp16 tiles, once for both row tiles.  The
+// two row tiles take turns: while one's rows are in the softmax, the tensor
+// core works for the other.
+//
+// The products are exact (codes and power-of-two scaled queries are fp16),
+// sums fp32.  A page's value scale joins its logits instead of its values:
+//   y_j = x_j + log2(vs / vref),  P_j = 2^(y_j - m),  m >= max y - kSlack,
+// so P_j vcode_j vref is p_j vs vcode_j in the row's own units, whatever the
+// scales; the softmax sum takes P_j (vref / vs) page by page.  P is rounded
+// once to fp16, 2^kChunkBias at m: 2^-11 of a weight, down to 2^-34 of the
+// largest.  m follows the running maximum only when that has grown by more
+// than kSlack, so O is rarely rescaled.
+//
+// Bound: 128 x 128 weights take 1,024 clocks of the exponential unit and
+// their two products the same of the tensor core; the conversion's share of
+// the issue slots is halved by the two row tiles.
+#pragma once
+
+#include "kv8_attn.cuh"
+#include "tcgen05.cuh"
+
+namespace csa2 {
+namespace kv8 {
+
+using namespace tc;
+
+constexpr int kChunkKeys = 128;
+constexpr int kChunkRows = 256;
+constexpr int kSoftWarps = 8;
+constexpr int kConvWarps = 4;  // 13 warps: 128 registers a thread
+constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr float kChunkBias = 10.f, kSlack = 5.f;  // 2^(10 + 5) < 65504
+constexpr int kMetaSlots = 4;
+
+template <int D>
+struct ChunkShape {
+  static constexpr int DH = D / 64;          // 128-byte wide sub-tiles of a row
+  static constexpr int SUB = 128 * 128;      // bytes of a sub-tile of 128 rows
+  static constexpr int TILE = DH * SUB;
+  static constexpr size_t PART = size_t(kChunkRows) * (D + 2);  // floats of one partial
+};
+
+struct ChunkMeta {
+  float ks[8], lvs[8], ivs[8];
+};
+
+template <int D>
+struct ChunkSmem {
+  alignas(1024) uint8_t q[2][ChunkShape<D>::TILE];
+  alignas(1024) uint8_t k[2][ChunkShape<D>::TILE];
+  alignas(1024) uint8_t v[2][ChunkShape<D>::TILE];
+  ChunkMeta meta[kMetaSlots];
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t meta_full[kMetaSlots], drained;
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag;
+  long long sum[kChunkThreads / 32];
+  long long pre;
+  int b;
+};
+
+template <int D>
+constexpr size_t chunk_smem_bytes() {
+  return sizeof(ChunkSmem<D>) + 1024 < 120 * 1024 ? 120 * 1024 : sizeof(ChunkSmem<D>) + 1024;
+}
+
+// Bounded wait that also gives up once another role has.
+template <int D>
+__device__ __forceinline__ bool chunk_wait(ChunkSmem<D> &sm, uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long start = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (sm.abort_flag) return false;
+    if (clock64() - start > (1ll << 32)) {
+      raise_status(kStatusWaitTimeout);
+      sm.abort_flag = 1u;
+      return false;
+    }
+  }
+  return true;
+}
+
+// Operand rows of 128 bytes, 128-byte swizzle, 8-row groups 1,024 bytes apart.
+// K-major: a k-step of 16 is 32 bytes on.  MN-major (values: 64 dims of a key
+// per row): `lead` bytes to the next 64 dims, 1,024 to the next 8 keys.
+__device__ __forceinline__ uint64_t chunk_desc(const void *smem, uint32_t lead) {
+  const uint64_t addr = smem_u32(smem);
+  return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// fp16 x fp16 -> fp32, M = 128, N = n; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t chunk_idesc(int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The wait that makes loaded TMEM values usable, tied to their registers.
+__device__ __forceinline__ void tmem_landed(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+  asm volatile(""
+               : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+                 "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// The line of steps (a tile's 128-key steps), cut evenly over the CTAs as in
+// kv8_attn.cuh.  A tile's steps end at its last row's position.
+// ---------------------------------------------------------------------------
+struct ChunkSeq {
+  int t0, T, pos0, tiles, reach;  // reach: positions that the table holds
+};
+
+__device__ __forceinline__ ChunkSeq chunk_seq(const AttnParams &p, int b) {
+  ChunkSeq s;
+  const int32_t lo = max(p.s.cu[b], 0), hi = p.s.cu[b + 1];
+  s.t0 = lo;
+  s.T = (int)max((int64_t)0, min64(hi, p.s.n) - lo);
+  s.pos0 = (int)max((int64_t)-0x40000000, (int64_t)p.s.lens[b] - hi + lo);
+  s.tiles = (int)(((int64_t)s.T * p.G + kChunkRows - 1) / kChunkRows);
+  s.reach = p.s.width << p.c.bs_shift;
+  return s;
+}
+
+__device__ __forceinline__ int chunk_steps(const ChunkSeq &s, int G, int x) {
+  const int rows = min((x + 1) * kChunkRows, s.T * G);
+  const int64_t seen = min64((int64_t)s.pos0 + (rows - 1) / G + 1, s.reach);
+  return max(1, (int)((seen + kChunkKeys - 1) / kChunkKeys));
+}
+
+struct ChunkWalk {
+  const AttnParams &p;
+  long long u, u1;   // the CTA's stretch from here on
+  ChunkSeq s;
+  int b, h, x;
+  int steps, first, last;  // of the tile; the CTA's steps of it are [first, last)
+  int row0, nrows, pos_first, pos_last;
+
+  __device__ ChunkWalk(const AttnParams &p_, long long u0_, long long u1_, int b_, long long pre)
+      : p(p_), u(u0_), u1(u1_), b(b_) {
+    s = chunk_seq(p, b);
+    long long per = 0;  // steps of the sequence per kv head
+    for (int i = 0; i < s.tiles; ++i) per += chunk_steps(s, p.G, i);
+    long long r = u - pre;
+    h = (int)(r / per);
+    r -= (long long)h * per;
+    for (x = 0; x < s.tiles - 1; ++x) {
+      const int n = chunk_steps(s, p.G, x);
+      if (r < n) break;
+      r -= n;
+    }
+    set((int)r);
+  }
+  __device__ void set(int from) {
+    steps = chunk_steps(s, p.G, x);
+    first = from;
+    last = (int)min64(steps, from + (u1 - u));
+    row0 = x * kChunkRows;
+    nrows = min(kChunkRows, s.T * p.G - row0);
+    pos_first = s.pos0 + row0 / p.G;
+    pos_last = s.pos0 + (row0 + nrows - 1) / p.G;
+  }
+  __device__ bool next() {
+    u += last - first;
+    if (u >= u1) return false;
+    if (++x >= s.tiles) {
+      x = 0;
+      if (++h >= p.c.Hk) {
+        h = 0;
+        do {
+          s = chunk_seq(p, ++b);
+        } while (s.tiles == 0 && b < p.s.B - 1);
+      }
+    }
+    set(0);
+    return true;
+  }
+};
+
+// Page of block j of sequence b, or -1: not seen, past the table, outside the
+// cache (recorded).
+__device__ __forceinline__ int chunk_page(const AttnParams &p, int b, int j, int pos_last) {
+  if ((int64_t)j << p.c.bs_shift > pos_last || j >= p.s.width) return -1;
+  const int page = p.s.table[(int64_t)b * p.s.width + j];
+  if (page >= 0 && page < p.c.pages) return page;
+  raise_status(kStatusBadIndex);
+  return -1;
+}
+
+// The unit of a sequence's values: the value scale of its first page.
+__device__ __forceinline__ float chunk_vref(const AttnParams &p, int b, int h) {
+  const int page = p.s.table[(int64_t)b * p.s.width];
+  const float v = page >= 0 && page < p.c.pages ? p.c.v_scale[page * p.c.Hk + h] : 1.f;
+  return v > 0.f && v < INFINITY ? v : 1.f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnParams p) {
+  using S = ChunkShape<D>;
+  extern __shared__ __align__(1024) unsigned char chunk_smem_raw[];
+  ChunkSmem<D> &sm = *reinterpret_cast<ChunkSmem<D> *>(
+      (reinterpret_cast<uintptr_t>(chunk_smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kWarps = kChunkThreads / 32;
+  pdl_allow_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], kSoftWarps / 2);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kSoftWarps / 2);
+      mbar_init(&sm.o_done[i], 1);
+      mbar_init(&sm.k_full[i], kConvWarps);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], kConvWarps);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sm.meta_full[i], 1);
+    mbar_init(&sm.drained, 1);
+    sm.abort_flag = 0u;
+    sm.b = 0;
+    sm.pre = 0;
+    fence_barrier_init();
+  }
+  // ---- this CTA's stretch of the line ----
+  long long mine = 0;
+  for (int b = tid; b < p.s.B; b += kChunkThreads) {
+    const ChunkSeq s = chunk_seq(p, b);
+    for (int x = 0; x < s.tiles; ++x) mine += chunk_steps(s, p.G, x);
+    if (s.tiles > 0 && blockIdx.x == 0 && p.s.lens[b] > s.reach) raise_status(kStatusBadIndex);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sm.sum[warp] = mine;
+  __syncthreads();
+  long long W = 0;
+  for (int w = 0; w < kWarps; ++w) W += sm.sum[w];
+  W *= p.c.Hk;
+  const long long ctas = max(1ll, min((long long)gridDim.x, (W + 1) / 2));
+  const long long c = blockIdx.x;
+  const long long u0 = c < ctas ? W * c / ctas : W, u1 = c < ctas ? W * (c + 1) / ctas : W;
+  if (u0 >= u1) {
+    if (tid == 0) p.rec[c] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  long long before = 0;
+  for (int b0 = 0; b0 < p.s.B; b0 += kChunkThreads) {
+    const int b = b0 + tid;
+    long long w = 0;
+    if (b < p.s.B) {
+      const ChunkSeq s = chunk_seq(p, b);
+      for (int x = 0; x < s.tiles; ++x) w += chunk_steps(s, p.G, x);
+      w *= p.c.Hk;
+    }
+    const long long incl = warp_incl_scan64(w);
+    __syncthreads();
+    if (lane == 31) sm.sum[warp] = incl;
+    __syncthreads();
+    long long base = before;
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) base += sm.sum[k];
+      before += sm.sum[k];
+    }
+    const long long lo = base + incl - w;
+    if (w > 0 && lo <= u0 && u0 < lo + w) {
+      sm.b = b;
+      sm.pre = lo;
+    }
+    if (before > u0) break;  // uniform
+  }
+  if (warp == kWarps - 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  ChunkWalk walk(p, u0, u1, sm.b, sm.pre);
+
+  if (warp < kSoftWarps) {
+    // ---------------- softmax: one thread per query row ----------------
+    const int tile = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_at = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_at + (uint32_t)(tile * 128);
+    const uint32_t t_o = tmem + lane_at + 256u + (uint32_t)(tile * D);
+    uint32_t n_steps = 0;    // of this tile so far: phases of s_full and o_done
+    int k_index = 0;         // steps of both tiles so far: slots of the page facts
+    int4 rec = make_int4(-1, 0, 0, 0);
+    const int np_shift = p.c.bs_shift;
+    do {
+      const bool whole = walk.first == 0 && walk.last == walk.steps;
+      if (tile * 128 >= walk.nrows) {  // warp-uniform: no row of this tile
+        k_index += walk.last - walk.first;
+        continue;
+      }
+      const int r = tile * 128 + row;
+      const int R = walk.row0 + min(r, walk.nrows - 1);
+      const int tok = R / p.G;
+      const int64_t head = (int64_t)walk.h * p.G + R - tok * p.G;
+      const int my_pos = min(walk.s.pos0 + tok, kNoPos - 1);
+      float f;  // logit per product, without the page's key scale
+      {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + (int64_t)(walk.s.t0 + tok) * p.q_stride + head * D);
+        uint4 w[D / 8];
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          w[i] = src[i];
+          const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            big = fmaxf(big, fabsf(__uint_as_float(ws[e] << 16)));
+            big = fmaxf(big, fabsf(__uint_as_float(ws[e] & 0xffff0000u)));
+          }
+        }
+        const uint32_t eb = __float_as_uint(big) >> 23;
+        const uint32_t sb = min((big > 0.f && eb < 255u) ? max(254u - eb, 1u) : 127u, 253u);
+        f = fabsf(p.sm_scale) * 1.44269504088896340736f * __uint_as_float((254u - sb) << 23);
+        const float down = copysignf(__uint_as_float(sb << 23), p.sm_scale);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {  // dims 0, 2, 1, 3 of each 4, as the codes
+          uint4 x;
+          x.x = pack_f16(__uint_as_float(w[i].x << 16) * down, __uint_as_float(w[i].y << 16) * down);
+          x.y = pack_f16(__uint_as_float(w[i].x & 0xffff0000u) * down,
+                         __uint_as_float(w[i].y & 0xffff0000u) * down);
+          x.z = pack_f16(__uint_as_float(w[i].z << 16) * down, __uint_as_float(w[i].w << 16) * down);
+          x.w = pack_f16(__uint_as_float(w[i].z & 0xffff0000u) * down,
+                         __uint_as_float(w[i].w & 0xffff0000u) * down);
+          *reinterpret_cast<uint4 *>(sm.q[tile] + (i >> 3) * S::SUB + row * 128 +
+                                     (((i & 7) ^ (row & 7)) << 4)) = x;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full[tile]);
+
+      float m = -INFINITY, l = 0.f;
+      for (int t = walk.first; t < walk.last; ++t, ++k_index, ++n_steps) {
+        const ChunkMeta &me = sm.meta[k_index % kMetaSlots];
+        // the products first: once they are there, the page facts of this very
+        // step are (a row tile that skipped steps could mistake an older phase)
+        bool ok = chunk_wait(sm, &sm.s_full[tile], n_steps & 1u);
+        ok = ok && chunk_wait(sm, &sm.meta_full[k_index % kMetaSlots],
+                              (uint32_t)(k_index / kMetaSlots) & 1u);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const int key0 = t * kChunkKeys;
+        const int seen = my_pos - key0;  // columns 0 .. seen are visible
+        const bool edge = __any_sync(0xffffffffu, seen < kChunkKeys - 1);
+        // ---- the row's maximum ----
+        float mx = m;
+        uint32_t a[32], b2[32];
+        tmem_ld32(t_s, a);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t(&v)[32] = (ch & 1) ? b2 : a;
+          tmem_landed(v);
+          if (ch < 3) tmem_ld32(t_s + 32 * (ch + 1), (ch & 1) ? a : b2);
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (ch * 32 + j > seen) v[j] = 0xff800000u;  // -inf
+          }
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            m0 = fmaxf(m0, __uint_as_float(v[j]));
+            m1 = fmaxf(m1, __uint_as_float(v[16 + j]));
+          }
+          const int p0 = (ch * 32) >> np_shift, p1 = (ch * 32 + 16) >> np_shift;
+          // a masked half (or one whose key scale is 0) must not turn into NaN
+          if (m0 > -INFINITY) mx = fmaxf(mx, fmaf(m0, f * me.ks[p0], me.lvs[p0]));
+          if (m1 > -INFINITY) mx = fmaxf(mx, fmaf(m1, f * me.ks[p1], me.lvs[p1]));
+        }
+        // ---- the unit of the weights ----
+        float corr = 1.f;
+        if (mx > m + kSlack || (m == -INFINITY && mx > -INFINITY)) {
+          corr = m == -INFINITY ? 1.f : ex2(m - mx);  // (no weights yet: nothing to rescale)
+          m = mx;
+        }
+        l *= corr;
+        if (t > walk.first && __any_sync(0xffffffffu, corr != 1.f)) {
+          ok = chunk_wait(sm, &sm.o_done[tile], (n_steps - 1) & 1u);  // the products so far
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            tmem_ld32(t_o + 32 * ch, a);
+            tmem_landed(a);
+            uint32_t lo[16], hi[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              lo[j] = __float_as_uint(__uint_as_float(a[j]) * corr);
+              hi[j] = __float_as_uint(__uint_as_float(a[16 + j]) * corr);
+            }
+            tmem_st16(t_o + 32 * ch, lo);
+            tmem_st16(t_o + 32 * ch + 16, hi);
+          }
+        }
+        // ---- weights over S, sums ----
+        const float zero = (m == -INFINITY ? 0.f : m) - kChunkBias;
+        tmem_ld32(t_s, a);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t(&v)[32] = (ch & 1) ? b2 : a;
+          tmem_landed(v);
+          if (ch < 3) tmem_ld32(t_s + 32 * (ch + 1), (ch & 1) ? a : b2);
+          uint32_t w[16];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int pg = (ch * 32 + half * 16) >> np_shift;
+            const float fk = f * me.ks[pg], add = me.lvs[pg] - zero;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const int col = half * 16 + j;
+              float x0 = fmaf(__uint_as_float(v[col]), fk, add);
+              float x1 = fmaf(__uint_as_float(v[col + 1]), fk, add);
+              if (edge) {
+                if (ch * 32 + col > seen) x0 = -INFINITY;
+                if (ch * 32 + col + 1 > seen) x1 = -INFINITY;
+              }
+              const float e0 = ex2(x0), e1 = ex2(x1);
+              sum += e0 + e1;
+              w[col / 2] = pack_f16(e0, e1);
+            }
+            l = fmaf(sum, me.ivs[pg], l);
+          }
+          tmem_st16(t_s + 16 * ch, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[tile]);
+      }
+      // ---- out ----
+      bool ok = chunk_wait(sm, &sm.o_done[tile], (n_steps - 1) & 1u);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const float vref = chunk_vref(p, walk.b, walk.h);
+      const bool mine_out = r < walk.nrows;
+      const int64_t at = (int64_t)(walk.s.t0 + tok) * (p.G * p.c.Hk) + head;
+      const float zero = m - kChunkBias;
+      float *part = p.part + (2 * c + (walk.first > 0 ? 0 : 1)) * S::PART;
+      const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref;
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t v[32];
+        tmem_ld32(t_o + 32 * ch, v);
+        tmem_landed(v);
+        if (mine_out) {
+          float y[32];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {  // columns 0, 2, 1, 3 of each 4
+            y[j] = __uint_as_float(v[j]) * mul;
+            y[j + 2] = __uint_as_float(v[j + 1]) * mul;
+            y[j + 1] = __uint_as_float(v[j + 2]) * mul;
+            y[j + 3] = __uint_as_float(v[j + 3]) * mul;
+          }
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = (uint32_t)__bfloat16_as_ushort(
+                           __float2bfloat16(l == 0.f ? 0.f : y[j + 2 * e])) |
+                       ((uint32_t)__bfloat16_as_ushort(
+                            __float2bfloat16(l == 0.f ? 0.f : y[j + 2 * e + 1]))
+                        << 16);
+              *reinterpret_cast<uint4 *>(p.out + at * D + 32 * ch + j) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4 *>(part + r * D + 32 * ch + j) =
+                  make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+          }
+        }
+      }
+      if (mine_out && whole && p.lse)
+        p.lse[at] = l == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(l));
+      if (mine_out && !whole) {
+        part[kChunkRows * D + r] = l == 0.f ? -INFINITY : zero;
+        part[kChunkRows * D + kChunkRows + r] = l;
+      }
+      if (!whole && tile == 0) {
+        if (walk.first > 0) {
+          rec.z = walk.last == walk.steps;   // this CTA ends a tile begun earlier
+        } else {                             // it begins one that later CTAs end
+          rec.x = walk.s.t0;
+          rec.y = walk.h | (walk.nrows << 8);
+          rec.w = walk.row0;
+        }
+      }
+      tc_fence_before();  // these reads come before the next tile's products
+    } while (walk.next());
+    if (tid == 0) p.rec[c] = rec;
+  } else if (warp < kSoftWarps + kConvWarps) {
+    // ---------------- codes -> fp16 tiles ----------------
+    const int cw = warp - kSoftWarps;
+    // 8 consecutive lanes store 2 rows x 4 places of a 128-byte line: no two
+    // in the same banks under the swizzle
+    constexpr int RPW = D == 128 ? 4 : 8;             // rows per warp and pass
+    constexpr int PASSES = kChunkKeys / (RPW * kConvWarps);
+    const int piece = D == 128 ? ((lane & 3) | ((lane >> 3) & 1) << 2) : (lane & 3);
+    const int sub = D == 128 ? (((lane >> 2) & 1) | ((lane >> 4) & 1) << 1) : (lane >> 2);
+    uint32_t flip;
+    asm volatile("mov.b32 %0, %1;" : "=r"(flip) : "n"(kFlip));
+    uint4 kr[PASSES], vr[PASSES];
+    int ph[PASSES];         // page and head of this thread's rows, -1: zeros
+    int t = walk.first;
+    bool more = true;
+    auto pages = [&]() {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int key = t * kChunkKeys + (i * kConvWarps + cw) * RPW + sub;
+        const int page = chunk_page(p, walk.b, key >> p.c.bs_shift, walk.pos_last);
+        ph[i] = page < 0 ? -1 : page * p.c.Hk + walk.h;
+      }
+    };
+    auto load = [&](const int8_t *codes, uint4 (&reg)[PASSES]) {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int key = t * kChunkKeys + (i * kConvWarps + cw) * RPW + sub;
+        reg[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        if (ph[i] >= 0)
+          reg[i] = *reinterpret_cast<const uint4 *>(
+              codes + (((int64_t)ph[i] << p.c.bs_shift) + (key & (p.c.bs - 1))) * D + piece * 16);
+      }
+    };
+    auto store = [&](uint8_t *tile, const uint4 (&reg)[PASSES], uint32_t zeros) {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int r = (i * kConvWarps + cw) * RPW + sub;
+        const uint32_t ws[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = codes_f16(ws[e], flip);
+          o[2 * e + 1] = codes_f16(ws[e] >> 8, flip);
+        }
+        if (zeros >> i & 1u) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = 0u;
+        }
+        uint8_t *line = tile + (piece >> 2) * S::SUB + r * 128;
+        const int at = (((piece & 3) * 2) ^ (r & 7)) << 4;
+        *reinterpret_cast<uint4 *>(line + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(line + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    };
+    pages();
+    load(p.c.k, kr);
+    load(p.c.v, vr);
+    for (int k_index = 0; more; ++k_index) {
+      const int slot = k_index & 1;
+      const uint32_t free_phase = (uint32_t)((k_index >> 1) - 1) & 1u;
+      uint32_t k_zero = 0u, v_zero = 0u;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        k_zero |= (ph[i] < 0 ? 1u : 0u) << i;
+        v_zero |= (ph[i] < 0 || p.c.v_scale[max(ph[i], 0)] == 0.f ? 1u : 0u) << i;
+      }
+      if (k_index >= 2 && !chunk_wait(sm, &sm.k_empty[slot], free_phase)) break;
+      if (cw == 0) {  // the pages' scales (slots: the softmax is never 4 steps behind)
+        ChunkMeta &me = sm.meta[k_index % kMetaSlots];
+        if (lane < (kChunkKeys >> p.c.bs_shift)) {
+          const int j = ((t * kChunkKeys) >> p.c.bs_shift) + lane;
+          const int page = chunk_page(p, walk.b, j, walk.pos_last);
+          const float vref = chunk_vref(p, walk.b, walk.h);
+          float ks = 0.f, lvs = -INFINITY, ivs = 0.f;
+          if (page >= 0) {
+            const int at = page * p.c.Hk + walk.h;
+            const float vs = p.c.v_scale[at];
+            ks = p.c.k_scale[at];
+            lvs = vs == 0.f ? 0.f : log2f(vs / vref);
+            ivs = vs == 0.f ? 1.f : vref / vs;
+          }
+          me.ks[lane] = ks;
+          me.lvs[lane] = lvs;
+          me.ivs[lane] = ivs;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.meta_full[k_index % kMetaSlots]);
+      }
+      store(sm.k[slot], kr, k_zero);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[slot]);
+      // the next step's place, and its keys on the way
+      int next_t = t + 1;
+      bool step_more = true;
+      if (next_t >= walk.last) {
+        step_more = walk.next();
+        next_t = walk.first;
+      }
+      t = next_t;
+      if (step_more) {
+        pages();
+        load(p.c.k, kr);
+      }
+      if (k_index >= 2 && !chunk_wait(sm, &sm.v_empty[slot], free_phase)) break;
+      store(sm.v[slot], vr, v_zero);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[slot]);
+      if (step_more) load(p.c.v, vr);
+      more = step_more;
+    }
+  } else if (lane == 0) {
+    // ---------------- products ----------------
+    constexpr uint32_t kIdQK = chunk_idesc(kChunkKeys, false), kIdPV = chunk_idesc(D, true);
+    uint32_t n_seg[2] = {0u, 0u}, n_p[2] = {0u, 0u};
+    int k_index = 0;
+    bool ok = true;
+    auto qk = [&](int tile, int slot) {
+#pragma unroll
+      for (int hd = 0; hd < S::DH; ++hd) {
+        const uint64_t a = chunk_desc(sm.q[tile] + hd * S::SUB, 16);
+        const uint64_t b = chunk_desc(sm.k[slot] + hd * S::SUB, 16);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          umma_f16_ss(tmem + (uint32_t)(tile * 128), a + 2 * s, b + 2 * s, kIdQK,
+                      hd + s > 0 ? 1u : 0u);
+      }
+      umma_commit(&sm.s_full[tile]);
+    };
+    auto pv = [&](int tile, int slot, bool more) {
+      const uint64_t b = chunk_desc(sm.v[slot], S::SUB);
+#pragma unroll
+      for (int s = 0; s < kChunkKeys / 16; ++s)
+        umma_f16_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * 128 + 8 * s),
+                    b + (uint64_t)(s * 2048 >> 4), kIdPV, more || s > 0 ? 1u : 0u);
+      umma_commit(&sm.o_done[tile]);
+    };
+    do {
+      const int n = walk.last - walk.first;
+      const int tiles = walk.nrows > 128 ? 2 : 1;
+      for (int i = 0; i < tiles && ok; ++i) ok = chunk_wait(sm, &sm.q_full[i], n_seg[i]++ & 1u);
+      for (int t = 0; t < n && ok; ++t, ++k_index) {
+        const int slot = k_index & 1;
+        const uint32_t phase = (uint32_t)(k_index >> 1) & 1u;
+        if (t == 0) {
+          if (!(ok = chunk_wait(sm, &sm.k_full[slot], phase))) break;
+          tc_fence_after();
+          for (int i = 0; i < tiles; ++i) qk(i, slot);
+          umma_commit(&sm.k_empty[slot]);
+        }
+        if (!(ok = chunk_wait(sm, &sm.v_full[slot], phase))) break;
+        const bool next = t + 1 < n;
+        for (int i = 0; i < tiles; ++i) {
+          if (!(ok = chunk_wait(sm, &sm.p_full[i], n_p[i]++ & 1u))) break;
+          tc_fence_after();
+          pv(i, slot, t > 0);
+          if (i == tiles - 1) umma_commit(&sm.v_empty[slot]);
+          if (next) {
+            if (i == 0 && !(ok = chunk_wait(sm, &sm.k_full[slot ^ 1],
+                                            (uint32_t)((k_index + 1) >> 1) & 1u)))
+              break;
+            tc_fence_after();
+            qk(i, slot ^ 1);
+            if (i == tiles - 1) umma_commit(&sm.k_empty[slot ^ 1]);
+          }
+        }
+      }
+    } while (ok && walk.next());
+    // every product done before the tensor memory is freed
+    umma_commit(&sm.drained);
+    mbar_wait_bounded(&sm.drained, 0u);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarps - 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+}  // namespace kv8
+}  // namespace csa2

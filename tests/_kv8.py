@@ -115,27 +115,28 @@ def attn(q, c, table, cu, lens, sel=None, sm_scale=None):
 
     The third result is (A, S, N, M) per row: the mean of |value| under the
     softmax per dim, the largest sum of |q_d k_d| * scale over the keys, the
-    number of keys and the largest |value| per dim -- what an error bound
-    needs.  Padding rows are NaN."""
+    number of keys and the largest value that their pages' scales can hold
+    (127 max vs) -- what an error bound needs.  Padding rows are NaN."""
     P, Hk, bs, D = c["k"].shape
     n, H = q.shape[:2]
     G = H // Hk
     sm_scale = 1 / math.sqrt(D) if sm_scale is None else sm_scale
     out, lse = np.full((n, H, D), np.nan), np.full((n, H), np.nan)
     A, S, N = np.zeros((n, H, D)), np.zeros((n, H)), np.zeros((n, H))
-    M = np.zeros((n, H, D))
+    M = np.zeros((n, H))
     for i, b, pos in positions(cu, lens, n):
         if b < 0:
             continue
         nblk = pos // bs + 1 if pos >= 0 else 0
         for h in range(Hk):
             blocks = range(nblk) if sel is None else [j for j in sel[i, h] if 0 <= j < nblk]
-            ks, vs = [np.zeros((0, D))], [np.zeros((0, D))]
+            ks, vs, top = [np.zeros((0, D))], [np.zeros((0, D))], 0.0
             for j in blocks:
                 page = table[b, j] if j < table.shape[1] else -1
                 if page < 0 or page >= P:
                     continue
                 r = min(bs, pos + 1 - j * bs)
+                top = max(top, 127 * float(c["v_scale"][page, h]))
                 ks.append(c["k"][page, h, :r].astype(np.float64) * float(c["k_scale"][page, h]))
                 vs.append(c["v"][page, h, :r].astype(np.float64) * float(c["v_scale"][page, h]))
             k, v = np.concatenate(ks), np.concatenate(vs)
@@ -152,7 +153,7 @@ def attn(q, c, table, cu, lens, sel=None, sm_scale=None):
                 A[i, a] = p @ np.abs(v) / p.sum()
                 S[i, a] = (np.abs(k) @ np.abs(q[i, a].astype(np.float64))).max() * abs(sm_scale)
                 N[i, a] = len(k)
-                M[i, a] = np.abs(v).max(0)
+                M[i, a] = top
     return out, lse, (A, S, N, M)
 
 
@@ -163,17 +164,19 @@ def attn_bounds(out, lse, info):
     taken through exp2: |error| <= delta = (D + 8) 2^-24 S (any order of the
     sum, S the sum of magnitudes).  Weights are then off by a factor within
     1 +- (2 delta + 2^-20) and rounded once to fp16 (half a step, 2^-11); sums
-    of N terms in fp32 add N 2^-24.  The largest weight of a row is held as
-    2^14, so below 2^-28 of it a weight is an fp16 subnormal, whose half step
-    is 2^-25 / 2^14 = 2^-39 of the largest weight; the sum of weights is at
-    least the largest one, so the N weights of a row add at most N 2^-39 M.
+    of N terms in fp32 add N 2^-24.  The weights -- or weight times page scale,
+    in the kernel for many rows -- are held so that a row's largest is at least
+    2^10 (2^14 in the other kernel): below 2^-24 of it one is an fp16
+    subnormal, whose half step is 2^-25 / 2^10 = 2^-35 of the largest.  The sum
+    of weights is at least the largest weight and a code at most 127, so the N
+    weights of a row add at most N 2^-35 M.
     out is rounded once to bf16 (2^-8 of its value); lse once to fp32."""
     A, S, N, M = info
     D = out.shape[-1]
     delta = (D + 8) * 2.0 ** -24 * S
     rel = 2 * delta + 2.0 ** -20 + 2 * N * 2.0 ** -24
     tol_out = 2.0 ** -8 * np.abs(out) + (2.0 ** -11 + rel)[..., None] * A
-    tol_out += N[..., None] * 2.0 ** -39 * M + 1e-30
+    tol_out += (N * 2.0 ** -35 * M)[..., None] + 1e-30
     with np.errstate(invalid="ignore"):
         tol_lse = rel + 2.0 ** -22 * np.where(np.isfinite(lse), np.abs(lse), 0) + 2.0 ** -24
     return tol_out, tol_lse
