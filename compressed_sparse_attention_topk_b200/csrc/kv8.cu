@@ -83,6 +83,72 @@ csa2_status launch_append_d(const kv8::AppendParams &p, cudaStream_t st) {
   return after_launch();
 }
 
+// A dependent launch: its blocks come up while the kernel before it ends.
+template <class... Params, class... Args>
+csa2_status launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return CSA2_ERR_CUDA;
+  return after_launch();
+}
+
+template <int D, int R>
+void launch_score(const kv8::SelectParams &p, dim3 grid, cudaStream_t st) {
+  kv8::kv8_score_kernel<D, R><<<grid, kv8::kScoreThreads, 0, st>>>(p);
+}
+
+// Rows of more blocks than a warp's registers hold go to a CTA each, with
+// their keys in shared memory up to this many.
+constexpr int32_t kPickStaged = 40960;
+
+csa2_status launch_select(const kv8::SelectParams &p, cudaStream_t st) {
+  // tiles of 32 tokens where sequences have that many on average; the blocks
+  // split so that about four CTAs per SM share the work
+  const int32_t TT = p.s.n >= int64_t(32) * p.s.B ? 32 : 8;
+  const int64_t tiles = p.s.n / TT + p.s.B;
+  const int64_t most = std::max<int64_t>(1, ceil_div(p.s.width, 16 * kv8::kScoreWarps));
+  const int64_t splits = std::min<int64_t>(
+      std::min<int64_t>(most, 65535),
+      std::max<int64_t>(1, 4 * device_sms() / std::max<int64_t>(1, tiles * p.c.Hk)));
+  {
+    const dim3 grid((unsigned)tiles, (unsigned)p.c.Hk, (unsigned)splits);
+    TraceScope ts("kv8_score", st);
+    if (p.c.D == 64) TT == 8 ? launch_score<64, 1>(p, grid, st) : launch_score<64, 4>(p, grid, st);
+    else TT == 8 ? launch_score<128, 1>(p, grid, st) : launch_score<128, 4>(p, grid, st);
+    const csa2_status rc = after_launch();
+    if (rc != CSA2_OK) return rc;
+  }
+  const int64_t rows = p.s.n * p.c.Hk;
+  TraceScope ts("kv8_pick", st);
+  const dim3 warps((unsigned)ceil_div(rows, 4));
+  if (p.s.width <= 256)
+    return launch_dependent(kv8::kv8_pick_warp_kernel<8>, warps, 128, 0, st, p);
+  if (p.s.width <= 1024)
+    return launch_dependent(kv8::kv8_pick_warp_kernel<32>, warps, 128, 0, st, p);
+  if (p.s.width <= 2048)
+    return launch_dependent(kv8::kv8_pick_warp_kernel<64>, warps, 128, 0, st, p);
+  const int staged = p.s.width <= kPickStaged ? 1 : 0;
+  static std::atomic<bool> done[256];  // per device: attributes set
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 256 || !done[dev].load(std::memory_order_acquire)) {
+    if (set_smem_attr(kv8::kv8_pick_cta_kernel, size_t(kPickStaged) * 4, false) != CSA2_OK)
+      return CSA2_ERR_CUDA;
+    if (dev >= 0 && dev < 256) done[dev].store(true, std::memory_order_release);
+  }
+  return launch_dependent(kv8::kv8_pick_cta_kernel, dim3((unsigned)rows), kv8::kPickThreads,
+                          staged ? size_t(p.s.width) * 4 : 0, st, p, staged);
+}
+
 // The kernel of an attention call and its workspace.
 struct AttnPlan {
   bool chunk;      // 256-row tiles on tcgen05
@@ -112,18 +178,8 @@ AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
 template <int D, int ROWS>
 csa2_status launch_merge(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
   TraceScope ts("kv8_attn_merge", st);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.ctas, ROWS / 4);
-  cfg.blockDim = dim3(kv8::kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv8::kv8_merge_kernel<D, ROWS>, p, a.ctas) != cudaSuccess)
-    return CSA2_ERR_CUDA;
-  return after_launch();
+  return launch_dependent(kv8::kv8_merge_kernel<D, ROWS>, dim3((unsigned)a.ctas, ROWS / 4),
+                          kv8::kMergeThreads, 0, st, p, a.ctas);
 }
 
 template <int D>
@@ -281,7 +337,8 @@ csa2_status csa2_kv8_select(const uint16_t *q, int64_t q_stride, const csa2_kv8 
   rc = check_step(q, q_stride, p.c, table, width, cu, lens, B, H);
   if (rc != CSA2_OK) return rc;
   if (!sel || !aligned(sel, 4)) return CSA2_ERR_INVALID_ARG;
-  if (n_sel > 4096 || width > 65536 || n >= (int64_t(1) << 31)) return CSA2_ERR_UNSUPPORTED;
+  if (n_sel > 4096 || width > 65536 || n >= (int64_t(1) << 31) / p.c.Hk)
+    return CSA2_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < csa2_kv8_select_workspace_size(n, p.c.Hk, width) || !aligned(ws, 16))
     return CSA2_ERR_WORKSPACE;
   p.s = {cu, lens, table, B, width, n};
@@ -293,10 +350,7 @@ csa2_status csa2_kv8_select(const uint16_t *q, int64_t q_stride, const csa2_kv8 
   p.n_last = n_last;
   p.sel = sel;
   p.scores = static_cast<float *>(ws);
-  const dim3 grid((unsigned)std::min<int64_t>(n, 65535), (unsigned)p.c.Hk);
-  TraceScope ts("kv8_select", as_stream(stream));
-  kv8::kv8_select_kernel<<<grid, kv8::kSelectThreads, 0, as_stream(stream)>>>(p);
-  return after_launch();
+  return launch_select(p, as_stream(stream));
 }
 
 size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk, int32_t D,

@@ -1,6 +1,18 @@
 // Blocks of the 8-bit cache chosen for each token by a cheap score: the dot
 // of the token's int8 group query with each block's sum of key codes
 // (contract of csa2_kv8_select in include/csa2.h).
+//
+// Two launches.  kv8_score_kernel forms every score a token sees,
+//   score_j = fl(sum_d q8[d] ksum_j[d]) * k_scale_j,
+// exactly: the int16 sums are 256 hi + lo with hi int8 and lo uint8, so a dot
+// is two exact int8 products on the tensor cores (mma.sync m16n8k32, 16
+// blocks x 8 tokens), 256 times the first plus the second (< 2^28).  A
+// sequence's sums (2 D bytes per block and head) are read once per 8 or 32
+// tokens; bound by those bytes for a few tokens, by the scores' own traffic
+// for a chunk.  kv8_pick_*_kernel then takes each row's n_sel best: a score is
+// ordered as an unsigned key, forced blocks get the largest key, and the
+// n_sel-th largest key is found by bisection within a warp (rows of up to
+// 2,048 blocks, keys in registers) or by digits over a CTA.  Both latency-bound.
 #pragma once
 
 #include "kv8_cache.cuh"
@@ -19,101 +31,366 @@ struct SelectParams {
   float *scores;   // [n, Hk, width]
 };
 
-constexpr int kSelectThreads = 256;
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
 
-// One CTA per token and kv head.
-__global__ void __launch_bounds__(kSelectThreads) kv8_select_kernel(const SelectParams p) {
-  __shared__ int8_t s_q[128];
-  __shared__ float s_red[8];
-  __shared__ uint32_t s_hist[256], s_scan[33], s_pick[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int D = p.c.D;
+template <bool A_UNSIGNED>
+__device__ __forceinline__ void mma_i8(int32_t (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                       uint32_t b1) {
+  if constexpr (A_UNSIGNED)
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+        "%9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+        "%9}, {%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Blocks that position pos sees in a table of `width` blocks.
+__device__ __forceinline__ int seen_blocks(int64_t pos, int shift, int width) {
+  return pos < 0 ? 0 : (int)min64((pos >> shift) + 1, width);
+}
+
+// grid (token tiles, kv heads, splits of the blocks).  Tiles of 8 R tokens of
+// one sequence: with f(b) = cu[b] / (8 R) + b, tiles f(b) .. f(b + 1) - 1
+// belong to sequence b (enough for its tokens; a last one may be empty).
+template <int D, int R>
+__global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const SelectParams p) {
+  constexpr int TT = 8 * R;
+  constexpr int KS = D / 32;       // k-steps
+  constexpr int LD = D + 32;       // bytes per token of q8: its reads meet no bank twice
+  __shared__ __align__(16) int8_t s_q[TT][LD];
+  __shared__ int s_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y;
-  for (int64_t i = blockIdx.x; i < p.s.n; i += gridDim.x) {
-    const int b = seq_of(p.s, i);
-    if (b < 0) return;  // only padding from here on
-    const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
-    const int nblk = pos < 0 ? 0 : (int)min64((pos >> p.c.bs_shift) + 1, p.s.width);
-    // the group's query, in 8 bits
-    float qs = 0.f;
-    if (tid < D) {
-      double sum = 0.0;
-      for (int g = 0; g < p.G; ++g)
-        sum += (double)bf16_to_f32_bits(p.q[i * p.q_stride + (int64_t)(h * p.G + g) * D + tid]);
-      qs = (float)sum;
-    }
-    const float wm = warp_max(fabsf(qs) == fabsf(qs) ? fabsf(qs) : INFINITY);
-    if (lane == 0) s_red[warp] = wm;
-    __syncthreads();
-    float big = 0.f;
-    for (int w = 0; w < 8; ++w) big = fmaxf(big, s_red[w]);
-    const bool dead = !(big > 0.f && big < INFINITY);
-    if (tid < D)
-      s_q[tid] = dead ? (int8_t)0 : (int8_t)__float2int_rn(__fmul_rn(qs, __fdiv_rn(127.f, big)));
-    __syncthreads();
-    // scores
-    float *row = p.scores + (i * p.c.Hk + h) * p.s.width;
-    const int first = min(p.n_first, nblk);
-    const int last = max(first, nblk - p.n_last);  // candidates: [first, last)
-    for (int j = first + tid; j < last; j += kSelectThreads) {
-      const int32_t page = p.s.table[(int64_t)b * p.s.width + j];
-      float sc = -INFINITY;
-      if (page < 0 || page >= p.c.pages) {
-        raise_status(kStatusBadIndex);
-      } else {
-        const int64_t ph = (int64_t)page * p.c.Hk + h;
-        const int16_t *ks = p.c.k_sum + ph * D;
-        int dot = 0;
-        for (int d = 0; d < D; ++d) dot += (int)s_q[d] * ks[d];
-        sc = __fadd_rn(__fmul_rn((float)dot, p.c.k_scale[ph]), 0.f);
-      }
-      row[j] = sc;
-    }
-    __syncthreads();
-    // the want-th largest candidate by radix selection, 8 bits at a time
-    const int want = min(p.n_sel - (first + nblk - last), last - first);
-    uint32_t prefix = 0u, need = (uint32_t)want;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-      s_hist[tid] = 0u;
-      __syncthreads();
-      for (int j = first + tid; j < last; j += kSelectThreads) {
-        const uint32_t k = score_key(row[j]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&s_hist[(k >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      radix_threshold<kSelectThreads, 256>(s_hist, need, s_scan, s_pick);
-      prefix |= s_pick[0] << shift;
-      need -= s_pick[1];
-      __syncthreads();
-    }
-    // kept blocks in ascending order: candidates above the threshold, and the
-    // lowest `need` of those at it
-    int32_t *out = p.sel + (i * p.c.Hk + h) * p.n_sel;
-    uint32_t at = 0u, ties = 0u;
-    for (int j0 = 0; j0 < nblk; j0 += kSelectThreads) {
-      const int j = j0 + tid;
-      uint32_t keep = 0u, tie = 0u;
+  pdl_allow_dependents();
+  if (tid == 0) s_b = -1;
+  __syncthreads();
+  for (int b = tid; b < p.s.B; b += kScoreThreads) {
+    const int lo = p.s.cu[b] / TT + b, hi = p.s.cu[b + 1] / TT + b + 1;
+    if (lo <= (int)blockIdx.x && (int)blockIdx.x < hi) s_b = b;
+  }
+  __syncthreads();
+  const int b = s_b;
+  if (b < 0) return;
+  const int cu0 = max(p.s.cu[b], 0), cu1 = p.s.cu[b + 1];
+  const int64_t T = min64(cu1, p.s.n) - cu0;
+  const int64_t x0 = (int64_t)((int)blockIdx.x - (cu0 / TT + b)) * TT;  // first token
+  if (x0 < 0 || x0 >= T) return;
+  const int count = (int)min64(TT, T - x0);
+  const int64_t tok0 = cu0 + x0;
+  const int64_t pos_last = (int64_t)p.s.lens[b] - cu1 + tok0 + count - 1;
+  const int nblk = seen_blocks(pos_last, p.c.bs_shift, p.s.width);
+  const int groups = (nblk + 15) / 16;
+  const int stride = kScoreWarps * gridDim.z;
+  int gi = blockIdx.z * kScoreWarps + warp;
+
+  // this thread's two blocks of group gi: their page and head, or -1
+  int ph[2];
+  auto pages = [&](int grp) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int j = grp * 16 + g + 8 * e;
+      ph[e] = -1;
       if (j < nblk) {
-        if (j < first || j >= last) {
-          keep = 1u;
-        } else if (want > 0) {
-          const uint32_t k = score_key(row[j]);
-          keep = k > prefix ? 1u : 0u;
-          tie = k == prefix ? 1u : 0u;
+        const int page = p.s.table[(int64_t)b * p.s.width + j];
+        if (page >= 0 && page < p.c.pages) ph[e] = page * p.c.Hk + h;
+        else raise_status(kStatusBadIndex);
+      }
+    }
+  };
+  uint4 x[2][KS];
+  float ks[2];
+  auto load = [&]() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ks[e] = ph[e] >= 0 ? p.c.k_scale[ph[e]] : 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        x[e][s] = make_uint4(0u, 0u, 0u, 0u);
+        if (ph[e] >= 0)
+          x[e][s] = *reinterpret_cast<const uint4 *>(p.c.k_sum + (int64_t)ph[e] * D +
+                                                     (4 * s + t) * 8);
+      }
+    }
+  };
+  if (gi < groups) {
+    pages(gi);
+    load();
+  }
+
+  // ---- the tokens' group queries in 8 bits ----
+  for (int i = warp; i < TT; i += kScoreWarps) {
+    float qs[D / 32];
+    float big = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) qs[e] = 0.f;
+    if (i < count) {
+      double sum[D / 32];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) sum[e] = 0.0;
+      const uint16_t *src = p.q + (tok0 + i) * p.q_stride + (int64_t)h * p.G * D + lane * (D / 32);
+      for (int k = 0; k < p.G; ++k) {
+        uint32_t w[D / 64];
+        if constexpr (D == 128) {
+          const uint2 y = *reinterpret_cast<const uint2 *>(src + (int64_t)k * D);
+          w[0] = y.x;
+          w[D / 64 - 1] = y.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t *>(src + (int64_t)k * D);
+        }
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+          sum[2 * e] += (double)__uint_as_float(w[e] << 16);
+          sum[2 * e + 1] += (double)__uint_as_float(w[e] & 0xffff0000u);
         }
       }
-      uint32_t total;
-      const uint32_t before = block_excl_scan<kSelectThreads>(tie, s_scan, total);
-      if (tie && ties + before < need) keep = 1u;
-      ties += total;
-      const uint32_t o = block_excl_scan<kSelectThreads>(keep, s_scan, total);
-      if (keep && at + o < (uint32_t)p.n_sel) out[at + o] = j;
-      at += total;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        qs[e] = (float)sum[e];
+        const float a = fabsf(qs[e]);
+        big = fmaxf(big, a == a ? a : INFINITY);
+      }
     }
-    for (uint32_t o = at + tid; o < (uint32_t)p.n_sel; o += kSelectThreads) out[o] = -1;
-    __syncthreads();
+    big = warp_max(big);
+    const bool dead = !(big > 0.f && big < INFINITY);
+    const float r = dead ? 0.f : __fdiv_rn(127.f, big);
+    uint32_t word = 0u;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      const int q8 = dead ? 0 : __float2int_rn(__fmul_rn(qs[e], r));
+      word |= (uint32_t)(uint8_t)(int8_t)q8 << (8 * e);
+    }
+    if constexpr (D == 128) *reinterpret_cast<uint32_t *>(&s_q[i][lane * 4]) = word;
+    else *reinterpret_cast<uint16_t *>(&s_q[i][lane * 2]) = (uint16_t)word;
   }
+  __syncthreads();
+  uint32_t qb[R][KS][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint2 y = *reinterpret_cast<const uint2 *>(&s_q[r * 8 + g][(4 * s + t) * 8]);
+      qb[r][s][0] = y.x;
+      qb[r][s][1] = y.y;
+    }
+
+  // ---- 16 blocks at a time ----
+  for (; gi < groups; gi += stride) {
+    int32_t hi[R][4], lo[R][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hi[r][e] = lo[r][e] = 0;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      // bytes of dims 0..3 (first word) and 4..7 of the thread's 8
+      const uint32_t al[4] = {__byte_perm(x[0][s].x, x[0][s].y, 0x6420),
+                              __byte_perm(x[1][s].x, x[1][s].y, 0x6420),
+                              __byte_perm(x[0][s].z, x[0][s].w, 0x6420),
+                              __byte_perm(x[1][s].z, x[1][s].w, 0x6420)};
+      const uint32_t ah[4] = {__byte_perm(x[0][s].x, x[0][s].y, 0x7531),
+                              __byte_perm(x[1][s].x, x[1][s].y, 0x7531),
+                              __byte_perm(x[0][s].z, x[0][s].w, 0x7531),
+                              __byte_perm(x[1][s].z, x[1][s].w, 0x7531)};
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mma_i8<true>(lo[r], al, qb[r][s][0], qb[r][s][1]);
+        mma_i8<false>(hi[r], ah, qb[r][s][0], qb[r][s][1]);
+      }
+    }
+    const int j0 = gi * 16 + g;
+    const float k0 = ks[0], k1 = ks[1];
+    const bool bad0 = ph[0] < 0, bad1 = ph[1] < 0;
+    if (gi + stride < groups) {
+      pages(gi + stride);
+      load();
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r * 8 + 2 * t + (e & 1), j = j0 + (e >> 1) * 8;
+        if (i < count && j < nblk) {
+          const float dot = (float)(hi[r][e] * 256 + lo[r][e]);
+          const float sc = __fadd_rn(__fmul_rn(dot, (e >> 1) ? k1 : k0), 0.f);
+          p.scores[((tok0 + i) * p.c.Hk + h) * p.s.width + j] =
+              ((e >> 1) ? bad1 : bad0) ? -INFINITY : sc;
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The n_sel best of a row.
+// ---------------------------------------------------------------------------
+// Key of block j of nblk: 0 when there is none, the largest for a block that
+// is always kept.
+__device__ __forceinline__ uint32_t pick_key(const SelectParams &p, const float *row, int j,
+                                             int nblk) {
+  if (j >= nblk) return 0u;
+  if (j < p.n_first || j >= nblk - p.n_last) return 0xffffffffu;
+  return max(score_key(row[j]), 1u);
+}
+
+// One warp per row of up to 32 K blocks; lane l holds blocks 32 i + l.
+template <int K>
+__global__ void __launch_bounds__(128) kv8_pick_warp_kernel(const SelectParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int64_t i = item / p.c.Hk;
+  if (i >= p.s.n) return;
+  const int b = seq_of(p.s, i);
+  if (b < 0) return;
+  const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
+  const int nblk = seen_blocks(pos, p.c.bs_shift, p.s.width);
+  pdl_wait_primary();
+  const float *row = p.scores + item * p.s.width;
+  int32_t *out = p.sel + item * p.n_sel;
+  const int want = min(p.n_sel, nblk);
+  uint32_t key[K];
+  uint32_t top = 0u;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    key[k] = pick_key(p, row, k * 32 + lane, nblk);
+    top = max(top, key[k]);
+  }
+  // lo: at least `want` keys reach it; hi: fewer do.  Up to 32 wanted, the
+  // smallest of the lanes' largest keys is such a lo.
+  uint32_t lo = want <= 32 ? max(__reduce_min_sync(0xffffffffu, top), 1u) : 1u;
+  uint64_t hi = (uint64_t)__reduce_max_sync(0xffffffffu, top) + 1;
+  uint32_t above = 0u;  // keys that reach hi
+  bool ties = true;
+  while (hi - lo > 1) {
+    const uint32_t mid = (uint32_t)((lo + hi) >> 1);
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) n += key[k] >= mid ? 1u : 0u;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= (uint32_t)want) {
+      lo = mid;
+      if (n == (uint32_t)want) {
+        ties = false;
+        break;
+      }
+    } else {
+      hi = mid;
+      above = n;
+    }
+  }
+  // kept, in ascending order: keys that reach lo, of those that equal it the
+  // lowest blocks only
+  uint32_t left = ties ? (uint32_t)want - above : 0xffffffffu;
+  int at = 0;
+  const uint32_t lt = lanemask_lt_u32();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    bool keep = key[k] >= lo;
+    if (ties) {
+      const bool eq = key[k] == lo;
+      const uint32_t who = __ballot_sync(0xffffffffu, eq);
+      if (eq) keep = (uint32_t)__popc(who & lt) < left;
+      left -= min(left, (uint32_t)__popc(who));
+    }
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) out[at + __popc(kept & lt)] = k * 32 + lane;
+    at += __popc(kept);
+  }
+  for (int o = at + lane; o < p.n_sel; o += 32) out[o] = -1;
+}
+
+// One CTA per row: the threshold by three digits (11, 11 and 10 bits), each
+// from a histogram of the keys that share the digits so far.
+constexpr int kPickThreads = 512;
+
+__global__ void __launch_bounds__(kPickThreads) kv8_pick_cta_kernel(const SelectParams p,
+                                                                   int staged) {
+  extern __shared__ uint32_t pick_smem[];  // the row's keys, when they fit
+  __shared__ uint32_t s_hist[kBins1], s_scan[33], s_out[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t item = blockIdx.x;
+  const int64_t i = item / p.c.Hk;
+  const int b = seq_of(p.s, i);
+  if (b < 0) return;
+  const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
+  const int nblk = seen_blocks(pos, p.c.bs_shift, p.s.width);
+  for (int k = tid; k < kBins1; k += kPickThreads) s_hist[k] = 0u;
+  pdl_wait_primary();
+  const float *row = p.scores + item * p.s.width;
+  int32_t *out = p.sel + item * p.n_sel;
+  const int want = min(p.n_sel, nblk);
+  __syncthreads();
+  for (int j = tid; j < nblk; j += kPickThreads) {
+    const uint32_t k = pick_key(p, row, j, nblk);
+    if (staged) pick_smem[j] = k;
+    atomicAdd(&s_hist[key_d1(k)], 1u);
+  }
+  __syncthreads();
+  auto key = [&](int j) { return staged ? pick_smem[j] : pick_key(p, row, j, nblk); };
+  uint32_t need = (uint32_t)want, thr;
+  radix_threshold<kPickThreads, kBins1>(s_hist, need, s_scan, s_out);
+  thr = s_out[0] << 21;
+  need -= s_out[1];
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int shift = pass == 0 ? 10 : 0, bins = pass == 0 ? kBins2 : kBins3;
+    __syncthreads();
+    for (int k = tid; k < bins; k += kPickThreads) s_hist[k] = 0u;
+    __syncthreads();
+    const int above = pass == 0 ? 21 : 10;
+    for (int j = tid; j < nblk; j += kPickThreads) {
+      const uint32_t k = key(j);
+      if (k >> above == thr >> above) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1u);
+    }
+    __syncthreads();
+    if (pass == 0) radix_threshold<kPickThreads, kBins2>(s_hist, need, s_scan, s_out);
+    else radix_threshold<kPickThreads, kBins3>(s_hist, need, s_scan, s_out);
+    thr |= s_out[0] << shift;
+    need -= s_out[1];
+  }
+  // each warp takes a run of blocks; one scan over the warps' counts of keys
+  // above the threshold and at it, then every warp writes its own
+  const int run = (((nblk + kPickThreads - 1) / kPickThreads)) * 32;
+  const int j0 = warp * run, j1 = min(nblk, j0 + run);
+  uint32_t n_gt = 0u, n_eq = 0u;
+  for (int j = j0 + lane; j < j1; j += 32) {
+    const uint32_t k = key(j);
+    n_gt += k > thr ? 1u : 0u;
+    n_eq += k == thr ? 1u : 0u;
+  }
+  n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+  __syncthreads();
+  if (lane == 0) {
+    s_hist[warp] = n_gt;
+    s_hist[64 + warp] = n_eq;
+  }
+  __syncthreads();
+  uint32_t at = 0u, eq = 0u;  // kept and equal ones before this warp's run
+  for (int w = 0; w < warp; ++w) {
+    at += s_hist[w];
+    eq += s_hist[64 + w];
+  }
+  at += min(eq, need);
+  const uint32_t lt = lanemask_lt_u32();
+  for (int base = j0; base < j1; base += 32) {
+    const int j = base + lane;
+    const uint32_t k = j < j1 ? key(j) : 0u;
+    const bool is_eq = j < j1 && k == thr;
+    const uint32_t who = __ballot_sync(0xffffffffu, is_eq);
+    const bool keep = (j < j1 && k > thr) || (is_eq && eq + __popc(who & lt) < need);
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) out[at + __popc(kept & lt)] = j;
+    at += __popc(kept);
+    eq += __popc(who);
+  }
+  for (int o = want + tid; o < p.n_sel; o += kPickThreads) out[o] = -1;
 }
 
 }  // namespace kv8
