@@ -125,8 +125,8 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
 }
 
 // The wait that makes loaded TMEM values usable, tied to their registers.
-__device__ __forceinline__ void tmem_landed(uint32_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
+__device__ __forceinline__ void tie(uint32_t (&v)[32]) {
+  asm volatile(""
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
                  "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
                  "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
@@ -135,15 +135,91 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&v)[32]) {
                  "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
                  "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+__device__ __forceinline__ void tmem_landed(uint32_t (&v)[32]) {
+  tmem_wait_ld();
+  tie(v);
+}
+__device__ __forceinline__ void tmem_landed(uint32_t (&v)[32], uint32_t (&w)[32]) {
+  tmem_wait_ld();
+  tie(v);
+  tie(w);
 }
 
+// Largest of 16 values: three-input maxima.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max16(const uint32_t *v) {
+  float m0 = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+  float m1 = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+  for (int j = 6; j < 14; j += 4) {
+    m0 = max3(m0, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+    m1 = max3(m1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+  }
+  m0 = max3(m0, __uint_as_float(v[14]), __uint_as_float(v[15]));
+  return fmaxf(m0, m1);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Weights of 16 columns of a row: 2^(s fk + add), packed as fp16 into w[0..7];
+// returns their sum.  EDGE: columns past `seen` (counted from the first) are
+// not seen.
+template <bool EDGE>
+__device__ __forceinline__ float weights16(const uint32_t *v, float fk, float add, int seen,
+                                           uint32_t *w) {
+  const uint64_t f2 = pack2(fk, fk), a2 = pack2(add, add);
+  uint64_t sum = pack2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    float x0, x1;
+    unpack2(fma2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2, a2), x0, x1);
+    if (EDGE) {
+      if (j > seen) x0 = -INFINITY;
+      if (j + 1 > seen) x1 = -INFINITY;
+    }
+    const float e0 = ex2(x0), e1 = ex2(x1);
+    sum = add2(sum, pack2(e0, e1));
+    w[j / 2] = pack_f16(e0, e1);
+  }
+  float s0, s1;
+  unpack2(sum, s0, s1);
+  return s0 + s1;
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
+}
 // ---------------------------------------------------------------------------
 // The line of steps (a tile's 128-key steps), cut evenly over the CTAs as in
 // kv8_attn.cuh.  A tile's steps end at its last row's position.
@@ -393,30 +469,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         const int key0 = t * kChunkKeys;
         const int seen = my_pos - key0;  // columns 0 .. seen are visible
         const bool edge = __any_sync(0xffffffffu, seen < kChunkKeys - 1);
-        // ---- the row's maximum ----
+        // ---- the row's maximum (two rounds of 64 columns: the code stays
+        // small enough for the instruction caches) ----
         float mx = m;
         uint32_t a[32], b2[32];
-        tmem_ld32(t_s, a);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t(&v)[32] = (ch & 1) ? b2 : a;
-          tmem_landed(v);
-          if (ch < 3) tmem_ld32(t_s + 32 * (ch + 1), (ch & 1) ? a : b2);
+#pragma unroll 1
+        for (int hf = 0; hf < 128; hf += 64) {
+          tmem_ld32(t_s + hf, a);
+          tmem_ld32(t_s + hf + 32, b2);
+          tmem_landed(a, b2);
           if (edge) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (ch * 32 + j > seen) v[j] = 0xff800000u;  // -inf
+            for (int j = 0; j < 32; ++j) {
+              if (hf + j > seen) a[j] = 0xff800000u;  // -inf
+              if (hf + 32 + j > seen) b2[j] = 0xff800000u;
+            }
           }
-          float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            m0 = fmaxf(m0, __uint_as_float(v[j]));
-            m1 = fmaxf(m1, __uint_as_float(v[16 + j]));
+          for (int part = 0; part < 4; ++part) {
+            const float top = max16((part & 2 ? b2 : a) + (part & 1) * 16);
+            const int pg = (hf + part * 16) >> np_shift;
+            // (a masked part must not turn into NaN under a key scale of 0)
+            if (top > -INFINITY) mx = fmaxf(mx, fmaf(top, f * me.ks[pg], me.lvs[pg]));
           }
-          const int p0 = (ch * 32) >> np_shift, p1 = (ch * 32 + 16) >> np_shift;
-          // a masked half (or one whose key scale is 0) must not turn into NaN
-          if (m0 > -INFINITY) mx = fmaxf(mx, fmaf(m0, f * me.ks[p0], me.lvs[p0]));
-          if (m1 > -INFINITY) mx = fmaxf(mx, fmaf(m1, f * me.ks[p1], me.lvs[p1]));
         }
         // ---- the unit of the weights ----
         float corr = 1.f;
@@ -429,50 +504,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
           ok = chunk_wait(sm, &sm.o_done[tile], (n_steps - 1) & 1u);  // the products so far
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
-#pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) {
-            tmem_ld32(t_o + 32 * ch, a);
+#pragma unroll 1
+          for (int ch = 0; ch < D; ch += 32) {
+            tmem_ld32(t_o + ch, a);
             tmem_landed(a);
-            uint32_t lo[16], hi[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              lo[j] = __float_as_uint(__uint_as_float(a[j]) * corr);
-              hi[j] = __float_as_uint(__uint_as_float(a[16 + j]) * corr);
-            }
-            tmem_st16(t_o + 32 * ch, lo);
-            tmem_st16(t_o + 32 * ch + 16, hi);
+            for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * corr);
+            tmem_st32(t_o + ch, a);
           }
         }
         // ---- weights over S, sums ----
         const float zero = (m == -INFINITY ? 0.f : m) - kChunkBias;
-        tmem_ld32(t_s, a);
+#pragma unroll 1
+        for (int hf = 0; hf < 128; hf += 64) {
+          tmem_ld32(t_s + hf, a);
+          tmem_ld32(t_s + hf + 32, b2);
+          tmem_landed(a, b2);
+          uint32_t w[32];
+          float fk[4], add[4], sum[4];
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t(&v)[32] = (ch & 1) ? b2 : a;
-          tmem_landed(v);
-          if (ch < 3) tmem_ld32(t_s + 32 * (ch + 1), (ch & 1) ? a : b2);
-          uint32_t w[16];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int pg = (ch * 32 + half * 16) >> np_shift;
-            const float fk = f * me.ks[pg], add = me.lvs[pg] - zero;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const int col = half * 16 + j;
-              float x0 = fmaf(__uint_as_float(v[col]), fk, add);
-              float x1 = fmaf(__uint_as_float(v[col + 1]), fk, add);
-              if (edge) {
-                if (ch * 32 + col > seen) x0 = -INFINITY;
-                if (ch * 32 + col + 1 > seen) x1 = -INFINITY;
-              }
-              const float e0 = ex2(x0), e1 = ex2(x1);
-              sum += e0 + e1;
-              w[col / 2] = pack_f16(e0, e1);
-            }
-            l = fmaf(sum, me.ivs[pg], l);
+          for (int part = 0; part < 4; ++part) {
+            const int pg = (hf + part * 16) >> np_shift;
+            fk[part] = f * me.ks[pg];
+            add[part] = me.lvs[pg] - zero;
           }
-          tmem_st16(t_s + 16 * ch, w);
+          if (edge) {
+#pragma unroll
+            for (int part = 0; part < 4; ++part)
+              sum[part] = weights16<true>((part & 2 ? b2 : a) + (part & 1) * 16, fk[part],
+                                          add[part], seen - hf - part * 16, w + part * 8);
+          } else {
+#pragma unroll
+            for (int part = 0; part < 4; ++part)
+              sum[part] = weights16<false>((part & 2 ? b2 : a) + (part & 1) * 16, fk[part],
+                                           add[part], 0, w + part * 8);
+          }
+#pragma unroll
+          for (int part = 0; part < 4; ++part)
+            l = fmaf(sum[part], me.ivs[(hf + part * 16) >> np_shift], l);
+          tmem_st32(t_s + hf / 2, w);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -489,7 +559,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const float zero = m - kChunkBias;
       float *part = p.part + (2 * c + (walk.first > 0 ? 0 : 1)) * S::PART;
       const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref;
-#pragma unroll
+#pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t v[32];
         tmem_ld32(t_o + 32 * ch, v);
