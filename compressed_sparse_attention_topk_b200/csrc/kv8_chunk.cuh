@@ -3,13 +3,14 @@
 // 5th-generation tensor cores.
 //
 // A CTA holds 256 query rows (token-major, the group's heads inside) of one
-// sequence and kv head as two 128-row tiles, and passes over its keys 128 at
-// a time.  Per step and tile: S = Q K^T (tcgen05, fp16 x fp16 -> fp32 in
-// TMEM), one thread per row takes the softmax and leaves the weights in TMEM
-// over S, O += P V (the weights as the TMEM operand).  Eight further warps
-// turn the next step's codes into fp16 tiles, once for both row tiles.  The
-// two row tiles take turns: while one's rows are in the softmax, the tensor
-// core works for the other.
+// sequence and kv head as two 128-row tiles, and passes over its keys 64 at a
+// time.  Per step and tile: S = Q K^T (tcgen05, fp16 x fp16 -> fp32 in TMEM),
+// one thread per row takes the softmax (its 64 logits in registers) and
+// leaves the weights in TMEM over S, O += P V (the weights as the TMEM
+// operand).  Four further warps turn the codes into fp16 tiles in shared
+// memory, up to four steps ahead, once for both row tiles.  S is double
+// buffered, so the products of the next step run while a tile's rows are in
+// the softmax.
 //
 // The products are exact (codes and power-of-two scaled queries are fp16),
 // sums fp32.  A page's value scale joins its logits instead of its values:
@@ -21,8 +22,7 @@
 // than kSlack, so O is rarely rescaled.
 //
 // Bound: 128 x 128 weights take 1,024 clocks of the exponential unit and
-// their two products the same of the tensor core; the conversion's share of
-// the issue slots is halved by the two row tiles.
+// their two products the same of the tensor core.
 #pragma once
 
 #include "kv8_attn.cuh"
@@ -33,34 +33,38 @@ namespace kv8 {
 
 using namespace tc;
 
-constexpr int kChunkKeys = 128;
+constexpr int kChunkKeys = 64;
+constexpr int kChunkGroups = kChunkKeys / 16;  // no page ends inside 16 positions
+constexpr int kChunkSlots = 4;                 // steps of fp16 tiles
 constexpr int kChunkRows = 256;
 constexpr int kSoftWarps = 8;
-constexpr int kConvWarps = 4;  // 13 warps: 128 registers a thread
+constexpr int kConvWarps = kChunkGroups;  // 13 warps: 128 registers a thread
 constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + 1);
 constexpr float kChunkBias = 10.f, kSlack = 5.f;  // 2^(10 + 5) < 65504
-constexpr int kMetaSlots = 4;
+constexpr int kMetaSlots = 8;
 
 template <int D>
 struct ChunkShape {
   static constexpr int DH = D / 64;          // 128-byte wide sub-tiles of a row
-  static constexpr int SUB = 128 * 128;      // bytes of a sub-tile of 128 rows
-  static constexpr int TILE = DH * SUB;
+  static constexpr int QSUB = 128 * 128;     // bytes of a sub-tile of the queries
+  static constexpr int SUB = kChunkKeys * 128;  // and of the keys or values
   static constexpr size_t PART = size_t(kChunkRows) * (D + 2);  // floats of one partial
 };
 
+// Scales of a step's groups of 16 positions: keys; values as log2(vs / vref)
+// and vref / vs.
 struct ChunkMeta {
-  float ks[8], lvs[8], ivs[8];
+  float ks[kChunkGroups], lvs[kChunkGroups], ivs[kChunkGroups];
 };
 
 template <int D>
 struct ChunkSmem {
-  alignas(1024) uint8_t q[2][ChunkShape<D>::TILE];
-  alignas(1024) uint8_t k[2][ChunkShape<D>::TILE];
-  alignas(1024) uint8_t v[2][ChunkShape<D>::TILE];
+  alignas(1024) uint8_t q[2][ChunkShape<D>::DH * ChunkShape<D>::QSUB];
+  alignas(1024) uint8_t k[kChunkSlots][ChunkShape<D>::DH * ChunkShape<D>::SUB];
+  alignas(1024) uint8_t v[kChunkSlots][ChunkShape<D>::DH * ChunkShape<D>::SUB];
   ChunkMeta meta[kMetaSlots];
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2];  // [row tile][buffer of S]
+  uint64_t k_full[kChunkSlots], k_empty[kChunkSlots], v_full[kChunkSlots], v_empty[kChunkSlots];
   uint64_t meta_full[kMetaSlots], drained;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
@@ -208,20 +212,29 @@ __device__ __forceinline__ float weights16(const uint32_t *v, float fk, float ad
   return s0 + s1;
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+// 16 columns, landed.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
-      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-      "r"(v[30]), "r"(v[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
-// The line of steps (a tile's 128-key steps), cut evenly over the CTAs as in
+// The line of steps (a tile's 64-key steps), cut evenly over the CTAs as in
 // kv8_attn.cuh.  A tile's steps end at its last row's position.
 // ---------------------------------------------------------------------------
 struct ChunkSeq {
@@ -323,15 +336,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], kSoftWarps / 2);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kSoftWarps / 2);
       mbar_init(&sm.o_done[i], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&sm.s_full[i][k], 1);
+        mbar_init(&sm.p_full[i][k], kSoftWarps / 2);
+      }
+    }
+    for (int i = 0; i < kChunkSlots; ++i) {
       mbar_init(&sm.k_full[i], kConvWarps);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], kConvWarps);
       mbar_init(&sm.v_empty[i], 1);
     }
-    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sm.meta_full[i], 1);
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sm.meta_full[i], kConvWarps);
     mbar_init(&sm.drained, 1);
     sm.abort_flag = 0u;
     sm.b = 0;
@@ -352,7 +369,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   long long W = 0;
   for (int w = 0; w < kWarps; ++w) W += sm.sum[w];
   W *= p.c.Hk;
-  const long long ctas = max(1ll, min((long long)gridDim.x, (W + 1) / 2));
+  const long long ctas = max(1ll, min((long long)gridDim.x, (W + 3) / 4));
   const long long c = blockIdx.x;
   const long long u0 = c < ctas ? W * c / ctas : W, u1 = c < ctas ? W * (c + 1) / ctas : W;
   if (u0 >= u1) {
@@ -402,12 +419,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     const int tile = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_at = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_at + (uint32_t)(tile * 128);
     const uint32_t t_o = tmem + lane_at + 256u + (uint32_t)(tile * D);
-    uint32_t n_steps = 0;    // of this tile so far: phases of s_full and o_done
+    uint32_t n_steps = 0;    // of this tile so far: buffers and phases
     int k_index = 0;         // steps of both tiles so far: slots of the page facts
     int4 rec = make_int4(-1, 0, 0, 0);
-    const int np_shift = p.c.bs_shift;
     do {
       const bool whole = walk.first == 0 && walk.last == walk.steps;
       if (tile * 128 >= walk.nrows) {  // warp-uniform: no row of this tile
@@ -448,7 +463,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
           x.z = pack_f16(__uint_as_float(w[i].z << 16) * down, __uint_as_float(w[i].w << 16) * down);
           x.w = pack_f16(__uint_as_float(w[i].z & 0xffff0000u) * down,
                          __uint_as_float(w[i].w & 0xffff0000u) * down);
-          *reinterpret_cast<uint4 *>(sm.q[tile] + (i >> 3) * S::SUB + row * 128 +
+          *reinterpret_cast<uint4 *>(sm.q[tile] + (i >> 3) * S::QSUB + row * 128 +
                                      (((i & 7) ^ (row & 7)) << 4)) = x;
         }
       }
@@ -461,37 +476,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         const ChunkMeta &me = sm.meta[k_index % kMetaSlots];
         // the products first: once they are there, the page facts of this very
         // step are (a row tile that skipped steps could mistake an older phase)
-        bool ok = chunk_wait(sm, &sm.s_full[tile], n_steps & 1u);
+        const uint32_t buf = n_steps & 1u, phase = (n_steps >> 1) & 1u;
+        bool ok = chunk_wait(sm, &sm.s_full[tile][buf], phase);
         ok = ok && chunk_wait(sm, &sm.meta_full[k_index % kMetaSlots],
                               (uint32_t)(k_index / kMetaSlots) & 1u);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const int key0 = t * kChunkKeys;
-        const int seen = my_pos - key0;  // columns 0 .. seen are visible
-        const bool edge = __any_sync(0xffffffffu, seen < kChunkKeys - 1);
-        // ---- the row's maximum (two rounds of 64 columns: the code stays
-        // small enough for the instruction caches) ----
-        float mx = m;
+        const uint32_t t_s = tmem + lane_at + (uint32_t)(tile * 128) + buf * 64u;
         uint32_t a[32], b2[32];
-#pragma unroll 1
-        for (int hf = 0; hf < 128; hf += 64) {
-          tmem_ld32(t_s + hf, a);
-          tmem_ld32(t_s + hf + 32, b2);
-          tmem_landed(a, b2);
+        tmem_ld32(t_s, a);
+        tmem_ld32(t_s + 32, b2);
+        const int seen = my_pos - t * kChunkKeys;  // columns 0 .. seen are visible
+        const bool edge = __any_sync(0xffffffffu, seen < kChunkKeys - 1);
+        float fk[4], lv[4];
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          fk[part] = f * me.ks[part];
+          lv[part] = me.lvs[part];
+        }
+        tmem_landed(a, b2);
+        // ---- the row's maximum ----
+        float mx = m;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          const uint32_t *v = (part & 2 ? b2 : a) + (part & 1) * 16;
+          float top;
           if (edge) {
+            top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (hf + j > seen) a[j] = 0xff800000u;  // -inf
-              if (hf + 32 + j > seen) b2[j] = 0xff800000u;
-            }
+            for (int j = 0; j < 16; ++j)
+              if (part * 16 + j <= seen) top = fmaxf(top, __uint_as_float(v[j]));
+          } else {
+            top = max16(v);
           }
-#pragma unroll
-          for (int part = 0; part < 4; ++part) {
-            const float top = max16((part & 2 ? b2 : a) + (part & 1) * 16);
-            const int pg = (hf + part * 16) >> np_shift;
-            // (a masked part must not turn into NaN under a key scale of 0)
-            if (top > -INFINITY) mx = fmaxf(mx, fmaf(top, f * me.ks[pg], me.lvs[pg]));
-          }
+          // (a masked part must not turn into NaN under a key scale of 0)
+          if (top > -INFINITY) mx = fmaxf(mx, fmaf(top, fk[part], lv[part]));
         }
         // ---- the unit of the weights ----
         float corr = 1.f;
@@ -505,49 +524,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int ch = 0; ch < D; ch += 32) {
-            tmem_ld32(t_o + ch, a);
-            tmem_landed(a);
+          for (int ch = 0; ch < D; ch += 16) {
+            uint32_t x[16];
+            tmem_ld16(t_o + ch, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * corr);
-            tmem_st32(t_o + ch, a);
+            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * corr);
+            tmem_st16(t_o + ch, x);
           }
         }
         // ---- weights over S, sums ----
         const float zero = (m == -INFINITY ? 0.f : m) - kChunkBias;
-#pragma unroll 1
-        for (int hf = 0; hf < 128; hf += 64) {
-          tmem_ld32(t_s + hf, a);
-          tmem_ld32(t_s + hf + 32, b2);
-          tmem_landed(a, b2);
-          uint32_t w[32];
-          float fk[4], add[4], sum[4];
 #pragma unroll
-          for (int part = 0; part < 4; ++part) {
-            const int pg = (hf + part * 16) >> np_shift;
-            fk[part] = f * me.ks[pg];
-            add[part] = me.lvs[pg] - zero;
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int part = half * 2 + e;
+            const uint32_t *v = (half ? b2 : a) + e * 16;
+            const float sum =
+                edge ? weights16<true>(v, fk[part], lv[part] - zero, seen - part * 16, w + e * 8)
+                     : weights16<false>(v, fk[part], lv[part] - zero, 0, w + e * 8);
+            l = fmaf(sum, me.ivs[part], l);
           }
-          if (edge) {
-#pragma unroll
-            for (int part = 0; part < 4; ++part)
-              sum[part] = weights16<true>((part & 2 ? b2 : a) + (part & 1) * 16, fk[part],
-                                          add[part], seen - hf - part * 16, w + part * 8);
-          } else {
-#pragma unroll
-            for (int part = 0; part < 4; ++part)
-              sum[part] = weights16<false>((part & 2 ? b2 : a) + (part & 1) * 16, fk[part],
-                                           add[part], 0, w + part * 8);
-          }
-#pragma unroll
-          for (int part = 0; part < 4; ++part)
-            l = fmaf(sum[part], me.ivs[(hf + part * 16) >> np_shift], l);
-          tmem_st32(t_s + hf / 2, w);
+          tmem_st16(t_s + 16 * half, w);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[tile]);
+        if (lane == 0) mbar_arrive(&sm.p_full[tile][buf]);
       }
       // ---- out ----
       bool ok = chunk_wait(sm, &sm.o_done[tile], (n_steps - 1) & 1u);
@@ -615,41 +619,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     if (tid == 0) p.rec[c] = rec;
   } else if (warp < kSoftWarps + kConvWarps) {
     // ---------------- codes -> fp16 tiles ----------------
+    // Warp cw has positions 16 cw .. of every step: one page.  8 consecutive
+    // lanes store 2 rows x 4 places of a 128-byte line: no two in the same
+    // banks under the swizzle.
     const int cw = warp - kSoftWarps;
-    // 8 consecutive lanes store 2 rows x 4 places of a 128-byte line: no two
-    // in the same banks under the swizzle
-    constexpr int RPW = D == 128 ? 4 : 8;             // rows per warp and pass
-    constexpr int PASSES = kChunkKeys / (RPW * kConvWarps);
+    constexpr int RPP = D == 128 ? 4 : 8;  // rows per pass
+    constexpr int PASSES = 16 / RPP;
     const int piece = D == 128 ? ((lane & 3) | ((lane >> 3) & 1) << 2) : (lane & 3);
     const int sub = D == 128 ? (((lane >> 2) & 1) | ((lane >> 4) & 1) << 1) : (lane >> 2);
     uint32_t flip;
     asm volatile("mov.b32 %0, %1;" : "=r"(flip) : "n"(kFlip));
     uint4 kr[PASSES], vr[PASSES];
-    int ph[PASSES];         // page and head of this thread's rows, -1: zeros
     int t = walk.first;
-    bool more = true;
-    auto pages = [&]() {
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int key = t * kChunkKeys + (i * kConvWarps + cw) * RPW + sub;
-        const int page = chunk_page(p, walk.b, key >> p.c.bs_shift, walk.pos_last);
-        ph[i] = page < 0 ? -1 : page * p.c.Hk + walk.h;
-      }
+    // page and head of this warp's positions of step t, -1: nothing there
+    auto page_of = [&]() {
+      const int page =
+          chunk_page(p, walk.b, (t * kChunkKeys + cw * 16) >> p.c.bs_shift, walk.pos_last);
+      return page < 0 ? -1 : page * p.c.Hk + walk.h;
     };
-    auto load = [&](const int8_t *codes, uint4 (&reg)[PASSES]) {
+    auto load = [&](const int8_t *codes, int ph, int at, uint4 (&reg)[PASSES]) {
+      const int r0 = (at * kChunkKeys + cw * 16) & (p.c.bs - 1);
+      const int8_t *src = codes + (((int64_t)max(ph, 0) << p.c.bs_shift) + r0 + sub) * D + piece * 16;
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int key = t * kChunkKeys + (i * kConvWarps + cw) * RPW + sub;
-        reg[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        if (ph[i] >= 0)
-          reg[i] = *reinterpret_cast<const uint4 *>(
-              codes + (((int64_t)ph[i] << p.c.bs_shift) + (key & (p.c.bs - 1))) * D + piece * 16);
-      }
+      for (int i = 0; i < PASSES; ++i)
+        reg[i] = ph < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                        : *reinterpret_cast<const uint4 *>(src + i * RPP * D);
     };
-    auto store = [&](uint8_t *tile, const uint4 (&reg)[PASSES], uint32_t zeros) {
+    auto store = [&](uint8_t *tile, const uint4 (&reg)[PASSES], bool zeros) {
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
-        const int r = (i * kConvWarps + cw) * RPW + sub;
+        const int r = cw * 16 + i * RPP + sub;
         const uint32_t ws[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
         uint32_t o[8];
 #pragma unroll
@@ -657,7 +656,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
           o[2 * e] = codes_f16(ws[e], flip);
           o[2 * e + 1] = codes_f16(ws[e] >> 8, flip);
         }
-        if (zeros >> i & 1u) {
+        if (zeros) {  // a value scale of 0: whatever the codes are
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = 0u;
         }
@@ -667,87 +666,76 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         *reinterpret_cast<uint4 *>(line + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     };
-    pages();
-    load(p.c.k, kr);
-    load(p.c.v, vr);
-    for (int k_index = 0; more; ++k_index) {
-      const int slot = k_index & 1;
-      const uint32_t free_phase = (uint32_t)((k_index >> 1) - 1) & 1u;
-      uint32_t k_zero = 0u, v_zero = 0u;
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        k_zero |= (ph[i] < 0 ? 1u : 0u) << i;
-        v_zero |= (ph[i] < 0 || p.c.v_scale[max(ph[i], 0)] == 0.f ? 1u : 0u) << i;
+    int ph = page_of();
+    float ks = ph >= 0 ? p.c.k_scale[ph] : 0.f, vs = ph >= 0 ? p.c.v_scale[ph] : 0.f;
+    float vref = chunk_vref(p, walk.b, walk.h);
+    load(p.c.k, ph, t, kr);
+    load(p.c.v, ph, t, vr);
+    for (int k_index = 0;; ++k_index) {
+      const int slot = k_index % kChunkSlots;
+      const uint32_t free_phase = (uint32_t)(k_index / kChunkSlots - 1) & 1u;
+      const bool v_zero = vs == 0.f;
+      const float lvs = ph < 0 ? -INFINITY : v_zero ? 0.f : log2f(vs / vref);
+      const float ivs = ph < 0 ? 0.f : v_zero ? 1.f : vref / vs;
+      // the next step's place; its page is on the way while this step is stored
+      bool more = true;
+      float next_vref = vref;
+      if (++t >= walk.last) {
+        more = walk.next();
+        t = walk.first;
+        if (more) next_vref = chunk_vref(p, walk.b, walk.h);
       }
-      if (k_index >= 2 && !chunk_wait(sm, &sm.k_empty[slot], free_phase)) break;
-      if (cw == 0) {  // the pages' scales (slots: the softmax is never 4 steps behind)
+      const int next_ph = more ? page_of() : -1;
+      if (k_index >= kChunkSlots && !chunk_wait(sm, &sm.k_empty[slot], free_phase)) break;
+      if (lane == 0) {  // (the softmax is never a ring of these behind)
         ChunkMeta &me = sm.meta[k_index % kMetaSlots];
-        if (lane < (kChunkKeys >> p.c.bs_shift)) {
-          const int j = ((t * kChunkKeys) >> p.c.bs_shift) + lane;
-          const int page = chunk_page(p, walk.b, j, walk.pos_last);
-          const float vref = chunk_vref(p, walk.b, walk.h);
-          float ks = 0.f, lvs = -INFINITY, ivs = 0.f;
-          if (page >= 0) {
-            const int at = page * p.c.Hk + walk.h;
-            const float vs = p.c.v_scale[at];
-            ks = p.c.k_scale[at];
-            lvs = vs == 0.f ? 0.f : log2f(vs / vref);
-            ivs = vs == 0.f ? 1.f : vref / vs;
-          }
-          me.ks[lane] = ks;
-          me.lvs[lane] = lvs;
-          me.ivs[lane] = ivs;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.meta_full[k_index % kMetaSlots]);
+        me.ks[cw] = ks;
+        me.lvs[cw] = lvs;
+        me.ivs[cw] = ivs;
+        mbar_arrive(&sm.meta_full[k_index % kMetaSlots]);
       }
-      store(sm.k[slot], kr, k_zero);
+      store(sm.k[slot], kr, false);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[slot]);
-      // the next step's place, and its keys on the way
-      int next_t = t + 1;
-      bool step_more = true;
-      if (next_t >= walk.last) {
-        step_more = walk.next();
-        next_t = walk.first;
-      }
-      t = next_t;
-      if (step_more) {
-        pages();
-        load(p.c.k, kr);
-      }
-      if (k_index >= 2 && !chunk_wait(sm, &sm.v_empty[slot], free_phase)) break;
+      load(p.c.k, next_ph, t, kr);
+      ks = next_ph >= 0 ? p.c.k_scale[next_ph] : 0.f;
+      vs = next_ph >= 0 ? p.c.v_scale[next_ph] : 0.f;
+      if (k_index >= kChunkSlots && !chunk_wait(sm, &sm.v_empty[slot], free_phase)) break;
       store(sm.v[slot], vr, v_zero);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[slot]);
-      if (step_more) load(p.c.v, vr);
-      more = step_more;
+      if (!more) break;
+      load(p.c.v, next_ph, t, vr);
+      ph = next_ph;
+      vref = next_vref;
     }
   } else if (lane == 0) {
     // ---------------- products ----------------
     constexpr uint32_t kIdQK = chunk_idesc(kChunkKeys, false), kIdPV = chunk_idesc(D, true);
-    uint32_t n_seg[2] = {0u, 0u}, n_p[2] = {0u, 0u};
+    uint32_t n_seg[2] = {0u, 0u}, n_s[2] = {0u, 0u}, n_p[2] = {0u, 0u};
     int k_index = 0;
     bool ok = true;
+    const uint64_t q_desc = chunk_desc(sm.q[0], 16), k_desc = chunk_desc(sm.k[0], 16);
+    const uint64_t v_desc = chunk_desc(sm.v[0], S::SUB);
     auto qk = [&](int tile, int slot) {
+      const uint32_t buf = n_s[tile]++ & 1u;
+      const uint64_t a = q_desc + (uint64_t)(tile * S::DH * S::QSUB >> 4);
+      const uint64_t b = k_desc + (uint64_t)(slot * S::DH * S::SUB >> 4);
 #pragma unroll
-      for (int hd = 0; hd < S::DH; ++hd) {
-        const uint64_t a = chunk_desc(sm.q[tile] + hd * S::SUB, 16);
-        const uint64_t b = chunk_desc(sm.k[slot] + hd * S::SUB, 16);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          umma_f16_ss(tmem + (uint32_t)(tile * 128), a + 2 * s, b + 2 * s, kIdQK,
-                      hd + s > 0 ? 1u : 0u);
-      }
-      umma_commit(&sm.s_full[tile]);
+      for (int s = 0; s < D / 16; ++s)
+        umma_f16_ss(tmem + (uint32_t)(tile * 128) + buf * 64u,
+                    a + (uint64_t)((s >> 2) * S::QSUB >> 4) + 2 * (s & 3),
+                    b + (uint64_t)((s >> 2) * S::SUB >> 4) + 2 * (s & 3), kIdQK, s > 0 ? 1u : 0u);
+      umma_commit(&sm.s_full[tile][buf]);
     };
-    auto pv = [&](int tile, int slot, bool more) {
-      const uint64_t b = chunk_desc(sm.v[slot], S::SUB);
+    auto pv = [&](int tile, int slot, uint32_t buf, bool more) {
+      const uint64_t b = v_desc + (uint64_t)(slot * S::DH * S::SUB >> 4);
 #pragma unroll
       for (int s = 0; s < kChunkKeys / 16; ++s)
-        umma_f16_ts(tmem + 256u + (uint32_t)(tile * D), tmem + (uint32_t)(tile * 128 + 8 * s),
+        umma_f16_ts(tmem + 256u + (uint32_t)(tile * D),
+                    tmem + (uint32_t)(tile * 128) + buf * 64u + (uint32_t)(8 * s),
                     b + (uint64_t)(s * 2048 >> 4), kIdPV, more || s > 0 ? 1u : 0u);
       umma_commit(&sm.o_done[tile]);
     };
@@ -755,31 +743,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const int n = walk.last - walk.first;
       const int tiles = walk.nrows > 128 ? 2 : 1;
       for (int i = 0; i < tiles && ok; ++i) ok = chunk_wait(sm, &sm.q_full[i], n_seg[i]++ & 1u);
-      for (int t = 0; t < n && ok; ++t, ++k_index) {
-        const int slot = k_index & 1;
-        const uint32_t phase = (uint32_t)(k_index >> 1) & 1u;
-        if (t == 0) {
-          if (!(ok = chunk_wait(sm, &sm.k_full[slot], phase))) break;
-          tc_fence_after();
-          for (int i = 0; i < tiles; ++i) qk(i, slot);
-          umma_commit(&sm.k_empty[slot]);
-        }
-        if (!(ok = chunk_wait(sm, &sm.v_full[slot], phase))) break;
+      for (int t = -1; t < n && ok; ++t) {
+        // the next step's logits before this one's weights are waited for
+        const int slot = k_index % kChunkSlots, next_slot = (k_index + 1) % kChunkSlots;
         const bool next = t + 1 < n;
+        const int k_slot = t < 0 ? slot : next_slot, k_at = t < 0 ? k_index : k_index + 1;
+        if (next && !(ok = chunk_wait(sm, &sm.k_full[k_slot], (uint32_t)(k_at / kChunkSlots) & 1u)))
+          break;
+        if (t >= 0 &&
+            !(ok = chunk_wait(sm, &sm.v_full[slot], (uint32_t)(k_index / kChunkSlots) & 1u)))
+          break;
+        tc_fence_after();
         for (int i = 0; i < tiles; ++i) {
-          if (!(ok = chunk_wait(sm, &sm.p_full[i], n_p[i]++ & 1u))) break;
-          tc_fence_after();
-          pv(i, slot, t > 0);
-          if (i == tiles - 1) umma_commit(&sm.v_empty[slot]);
           if (next) {
-            if (i == 0 && !(ok = chunk_wait(sm, &sm.k_full[slot ^ 1],
-                                            (uint32_t)((k_index + 1) >> 1) & 1u)))
-              break;
-            tc_fence_after();
-            qk(i, slot ^ 1);
-            if (i == tiles - 1) umma_commit(&sm.k_empty[slot ^ 1]);
+            qk(i, k_slot);
+            if (i == tiles - 1) umma_commit(&sm.k_empty[k_slot]);
           }
+          if (t < 0) continue;
+          const uint32_t buf = n_p[i] & 1u, phase = (n_p[i] >> 1) & 1u;
+          ++n_p[i];
+          if (!(ok = chunk_wait(sm, &sm.p_full[i][buf], phase))) break;
+          tc_fence_after();
+          pv(i, slot, buf, t > 0);
+          if (i == tiles - 1) umma_commit(&sm.v_empty[slot]);
         }
+        if (t >= 0) ++k_index;
       }
     } while (ok && walk.next());
     // every product done before the tensor memory is freed
