@@ -103,6 +103,18 @@ __device__ __forceinline__ uint64_t chunk_desc(const void *smem, uint32_t lead) 
          (1ull << 46) | (2ull << 61);
 }
 
+// One thread of a whole warp, chosen in a way that the compiler knows to be
+// one: the operands of the products then live in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // fp16 x fp16 -> fp32, M = 128, N = n; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t chunk_idesc(int n, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       ph = next_ph;
       vref = next_vref;
     }
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     // ---------------- products ----------------
     constexpr uint32_t kIdQK = chunk_idesc(kChunkKeys, false), kIdPV = chunk_idesc(D, true);
     uint32_t n_seg[2] = {0u, 0u}, n_s[2] = {0u, 0u}, n_p[2] = {0u, 0u};
