@@ -7,7 +7,7 @@
 // time.  Per step and tile: S = Q K^T (tcgen05, fp16 x fp16 -> fp32 in TMEM),
 // one thread per row takes the softmax (its 64 logits in registers) and
 // leaves the weights in TMEM over S, O += P V (the weights as the TMEM
-// operand).  Four further warps turn the codes into fp16 tiles in shared
+// operand).  Seven further warps turn the codes into fp16 tiles in shared
 // memory, up to four steps ahead, once for both row tiles.  S is double
 // buffered, so the products of the next step run while a tile's rows are in
 // the softmax.
@@ -38,7 +38,7 @@ constexpr int kChunkGroups = kChunkKeys / 16;  // no page ends inside 16 positio
 constexpr int kChunkSlots = 4;                 // steps of fp16 tiles
 constexpr int kChunkRows = 256;
 constexpr int kSoftWarps = 8;
-constexpr int kConvWarps = kChunkGroups;  // 13 warps: 128 registers a thread
+constexpr int kConvWarps = 7;  // with the products' 16 warps: 128 registers a thread
 constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + 1);
 constexpr float kChunkBias = 10.f, kSlack = 5.f;  // 2^(10 + 5) < 65504
 constexpr int kMetaSlots = 8;
@@ -63,7 +63,7 @@ struct ChunkSmem {
   alignas(1024) uint8_t k[kChunkSlots][ChunkShape<D>::DH * ChunkShape<D>::SUB];
   alignas(1024) uint8_t v[kChunkSlots][ChunkShape<D>::DH * ChunkShape<D>::SUB];
   ChunkMeta meta[kMetaSlots];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2];  // [row tile][buffer of S]
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];  // [row tile][buffer of S]
   uint64_t k_full[kChunkSlots], k_empty[kChunkSlots], v_full[kChunkSlots], v_empty[kChunkSlots];
   uint64_t meta_full[kMetaSlots], drained;
   uint32_t tmem_base;
@@ -200,21 +200,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // Weights of 16 columns of a row: 2^(s fk + add), packed as fp16 into w[0..7];
-// returns their sum.  EDGE: columns past `seen` (counted from the first) are
-// not seen.
-template <bool EDGE>
-__device__ __forceinline__ float weights16(const uint32_t *v, float fk, float add, int seen,
-                                           uint32_t *w) {
+// returns their sum.
+__device__ __forceinline__ float weights16(const uint32_t *v, float fk, float add, uint32_t *w) {
   const uint64_t f2 = pack2(fk, fk), a2 = pack2(add, add);
   uint64_t sum = pack2(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
     float x0, x1;
     unpack2(fma2(pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2, a2), x0, x1);
-    if (EDGE) {
-      if (j > seen) x0 = -INFINITY;
-      if (j + 1 > seen) x1 = -INFINITY;
-    }
     const float e0 = ex2(x0), e1 = ex2(x1);
     sum = add2(sum, pack2(e0, e1));
     w[j / 2] = pack_f16(e0, e1);
@@ -319,16 +312,6 @@ struct ChunkWalk {
   }
 };
 
-// Page of block j of sequence b, or -1: not seen, past the table, outside the
-// cache (recorded).
-__device__ __forceinline__ int chunk_page(const AttnParams &p, int b, int j, int pos_last) {
-  if ((int64_t)j << p.c.bs_shift > pos_last || j >= p.s.width) return -1;
-  const int page = p.s.table[(int64_t)b * p.s.width + j];
-  if (page >= 0 && page < p.c.pages) return page;
-  raise_status(kStatusBadIndex);
-  return -1;
-}
-
 // The unit of a sequence's values: the value scale of its first page.
 __device__ __forceinline__ float chunk_vref(const AttnParams &p, int b, int h) {
   const int page = p.s.table[(int64_t)b * p.s.width];
@@ -348,19 +331,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], kSoftWarps / 2);
-      mbar_init(&sm.o_done[i], 1);
       for (int k = 0; k < 2; ++k) {
         mbar_init(&sm.s_full[i][k], 1);
+        mbar_init(&sm.o_done[i][k], 1);
         mbar_init(&sm.p_full[i][k], kSoftWarps / 2);
       }
     }
     for (int i = 0; i < kChunkSlots; ++i) {
-      mbar_init(&sm.k_full[i], kConvWarps);
+      mbar_init(&sm.k_full[i], kChunkGroups);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], kConvWarps);
+      mbar_init(&sm.v_full[i], kChunkGroups);
       mbar_init(&sm.v_empty[i], 1);
     }
-    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sm.meta_full[i], kConvWarps);
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sm.meta_full[i], kChunkGroups);
     mbar_init(&sm.drained, 1);
     sm.abort_flag = 0u;
     sm.b = 0;
@@ -490,40 +473,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         // step are (a row tile that skipped steps could mistake an older phase)
         const uint32_t buf = n_steps & 1u, phase = (n_steps >> 1) & 1u;
         bool ok = chunk_wait(sm, &sm.s_full[tile][buf], phase);
-        ok = ok && chunk_wait(sm, &sm.meta_full[k_index % kMetaSlots],
-                              (uint32_t)(k_index / kMetaSlots) & 1u);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint32_t t_s = tmem + lane_at + (uint32_t)(tile * 128) + buf * 64u;
         uint32_t a[32], b2[32];
         tmem_ld32(t_s, a);
         tmem_ld32(t_s + 32, b2);
+        ok = chunk_wait(sm, &sm.meta_full[k_index % kMetaSlots],
+                        (uint32_t)(k_index / kMetaSlots) & 1u);
         const int seen = my_pos - t * kChunkKeys;  // columns 0 .. seen are visible
-        const bool edge = __any_sync(0xffffffffu, seen < kChunkKeys - 1);
         float fk[4], lv[4];
 #pragma unroll
         for (int part = 0; part < 4; ++part) {
-          fk[part] = f * me.ks[part];
+          // (never 0: a masked column's -inf must stay one)
+          fk[part] = fmaxf(f * me.ks[part], 1e-37f);
           lv[part] = me.lvs[part];
         }
         tmem_landed(a, b2);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (__any_sync(0xffffffffu, seen < kChunkKeys - 1)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j > seen) a[j] = 0xff800000u;  // -inf
+            if (j + 32 > seen) b2[j] = 0xff800000u;
+          }
+        }
         // ---- the row's maximum ----
         float mx = m;
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          const uint32_t *v = (part & 2 ? b2 : a) + (part & 1) * 16;
-          float top;
-          if (edge) {
-            top = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (part * 16 + j <= seen) top = fmaxf(top, __uint_as_float(v[j]));
-          } else {
-            top = max16(v);
-          }
-          // (a masked part must not turn into NaN under a key scale of 0)
-          if (top > -INFINITY) mx = fmaxf(mx, fmaf(top, fk[part], lv[part]));
-        }
+        for (int part = 0; part < 4; ++part)
+          mx = fmaxf(mx, fmaf(max16((part & 2 ? b2 : a) + (part & 1) * 16), fk[part], lv[part]));
         // ---- the unit of the weights ----
         float corr = 1.f;
         if (mx > m + kSlack || (m == -INFINITY && mx > -INFINITY)) {
@@ -532,7 +511,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         }
         l *= corr;
         if (t > walk.first && __any_sync(0xffffffffu, corr != 1.f)) {
-          ok = chunk_wait(sm, &sm.o_done[tile], (n_steps - 1) & 1u);  // the products so far
+          // the products so far
+          ok = chunk_wait(sm, &sm.o_done[tile][buf ^ 1u], ((n_steps - 1) >> 1) & 1u);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
 #pragma unroll 1
@@ -552,11 +532,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int part = half * 2 + e;
-            const uint32_t *v = (half ? b2 : a) + e * 16;
-            const float sum =
-                edge ? weights16<true>(v, fk[part], lv[part] - zero, seen - part * 16, w + e * 8)
-                     : weights16<false>(v, fk[part], lv[part] - zero, 0, w + e * 8);
-            l = fmaf(sum, me.ivs[part], l);
+            l = fmaf(weights16((half ? b2 : a) + e * 16, fk[part], lv[part] - zero, w + e * 8),
+                     me.ivs[part], l);
           }
           tmem_st16(t_s + 16 * half, w);
         }
@@ -566,7 +543,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         if (lane == 0) mbar_arrive(&sm.p_full[tile][buf]);
       }
       // ---- out ----
-      bool ok = chunk_wait(sm, &sm.o_done[tile], (n_steps - 1) & 1u);
+      // (a barrier per buffer: the products of the step before the last may be
+      // under way too, and one barrier's parity cannot tell the two apart)
+      bool ok = chunk_wait(sm, &sm.o_done[tile][(n_steps - 1) & 1u], ((n_steps - 1) >> 1) & 1u);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const float vref = chunk_vref(p, walk.b, walk.h);
@@ -631,36 +610,68 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     if (tid == 0) p.rec[c] = rec;
   } else if (warp < kSoftWarps + kConvWarps) {
     // ---------------- codes -> fp16 tiles ----------------
-    // Warp cw has positions 16 cw .. of every step: one page.  8 consecutive
-    // lanes store 2 rows x 4 places of a 128-byte line: no two in the same
-    // banks under the swizzle.
-    const int cw = warp - kSoftWarps;
+    // A task is 16 positions of one page, keys or values: eight to a step, keys
+    // first, dealt to the warps in turn.  8 consecutive lanes store 2 rows x 4
+    // places of a 128-byte line: no two in the same banks under the swizzle.
     constexpr int RPP = D == 128 ? 4 : 8;  // rows per pass
     constexpr int PASSES = 16 / RPP;
     const int piece = D == 128 ? ((lane & 3) | ((lane >> 3) & 1) << 2) : (lane & 3);
     const int sub = D == 128 ? (((lane >> 2) & 1) | ((lane >> 4) & 1) << 1) : (lane >> 2);
     uint32_t flip;
     asm volatile("mov.b32 %0, %1;" : "=r"(flip) : "n"(kFlip));
-    uint4 kr[PASSES], vr[PASSES];
-    int t = walk.first;
-    // page and head of this warp's positions of step t, -1: nothing there
-    auto page_of = [&]() {
-      const int page =
-          chunk_page(p, walk.b, (t * kChunkKeys + cw * 16) >> p.c.bs_shift, walk.pos_last);
-      return page < 0 ? -1 : page * p.c.Hk + walk.h;
+    uint4 reg[PASSES];
+    // Where a step's positions are: their page as the table has it (on the way
+    // from one iteration to the next), and what it takes to use it.
+    struct Place {
+      int step, part;      // part: 0 .. 3 keys, 4 .. 7 values
+      int raw, key, h;     // table entry, first position, kv head
+      bool seen;           // the entry was read: the positions are seen
+      float vref;
     };
-    auto load = [&](const int8_t *codes, int ph, int at, uint4 (&reg)[PASSES]) {
-      const int r0 = (at * kChunkKeys + cw * 16) & (p.c.bs - 1);
-      const int8_t *src = codes + (((int64_t)max(ph, 0) << p.c.bs_shift) + r0 + sub) * D + piece * 16;
+    int t = walk.first;
+    float vref_now = chunk_vref(p, walk.b, walk.h);
+    int step = 0, part = warp - kSoftWarps;  // of the task that `look` is at
+    auto look = [&](Place &at) {
+      at.step = step;
+      at.part = part;
+      at.key = t * kChunkKeys + (part % kChunkGroups) * 16;
+      const int j = at.key >> p.c.bs_shift;
+      at.h = walk.h;
+      at.vref = vref_now;
+      at.seen = (int64_t)j << p.c.bs_shift <= walk.pos_last && j < p.s.width;
+      at.raw = at.seen ? p.s.table[(int64_t)walk.b * p.s.width + j] : -1;
+    };
+    auto advance = [&]() {  // to this warp's next task; false: there is none
+      part += kConvWarps;
+      if (part < 2 * kChunkGroups) return true;
+      part -= 2 * kChunkGroups;
+      ++step;
+      if (++t < walk.last) return true;
+      if (!walk.next()) return false;
+      t = walk.first;
+      vref_now = chunk_vref(p, walk.b, walk.h);
+      return true;
+    };
+    // page and head, or -1 where nothing is seen or the page is not the cache's
+    auto page_head = [&](const Place &at) {
+      if (at.raw >= 0 && at.raw < p.c.pages) return at.raw * p.c.Hk + at.h;
+      if (at.seen && lane == 0) raise_status(kStatusBadIndex);
+      return -1;
+    };
+    auto load = [&](int ph, const Place &at) {
+      const int key = at.key;
+      const int8_t *src = (at.part < kChunkGroups ? p.c.k : p.c.v) +
+                          (((int64_t)max(ph, 0) << p.c.bs_shift) + (key & (p.c.bs - 1)) + sub) * D +
+                          piece * 16;
 #pragma unroll
       for (int i = 0; i < PASSES; ++i)
         reg[i] = ph < 0 ? make_uint4(0u, 0u, 0u, 0u)
                         : *reinterpret_cast<const uint4 *>(src + i * RPP * D);
     };
-    auto store = [&](uint8_t *tile, const uint4 (&reg)[PASSES], bool zeros) {
+    auto store = [&](uint8_t *tile, int row0, bool zeros) {
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
-        const int r = cw * 16 + i * RPP + sub;
+        const int r = row0 + i * RPP + sub;
         const uint32_t ws[4] = {reg[i].x, reg[i].y, reg[i].z, reg[i].w};
         uint32_t o[8];
 #pragma unroll
@@ -678,50 +689,44 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         *reinterpret_cast<uint4 *>(line + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     };
-    int ph = page_of();
+    Place here, there;  // of this step and of the next
+    look(here);
+    int ph = page_head(here);
+    bool more = advance();
+    if (more) look(there);
     float ks = ph >= 0 ? p.c.k_scale[ph] : 0.f, vs = ph >= 0 ? p.c.v_scale[ph] : 0.f;
-    float vref = chunk_vref(p, walk.b, walk.h);
-    load(p.c.k, ph, t, kr);
-    load(p.c.v, ph, t, vr);
-    for (int k_index = 0;; ++k_index) {
-      const int slot = k_index % kChunkSlots;
-      const uint32_t free_phase = (uint32_t)(k_index / kChunkSlots - 1) & 1u;
-      const bool v_zero = vs == 0.f;
-      const float lvs = ph < 0 ? -INFINITY : v_zero ? 0.f : log2f(vs / vref);
-      const float ivs = ph < 0 ? 0.f : v_zero ? 1.f : vref / vs;
-      // the next step's place; its page is on the way while this step is stored
-      bool more = true;
-      float next_vref = vref;
-      if (++t >= walk.last) {
-        more = walk.next();
-        t = walk.first;
-        if (more) next_vref = chunk_vref(p, walk.b, walk.h);
-      }
-      const int next_ph = more ? page_of() : -1;
-      if (k_index >= kChunkSlots && !chunk_wait(sm, &sm.k_empty[slot], free_phase)) break;
-      if (lane == 0) {  // (the softmax is never a ring of these behind)
-        ChunkMeta &me = sm.meta[k_index % kMetaSlots];
-        me.ks[cw] = ks;
-        me.lvs[cw] = lvs;
-        me.ivs[cw] = ivs;
-        mbar_arrive(&sm.meta_full[k_index % kMetaSlots]);
-      }
-      store(sm.k[slot], kr, false);
+    load(ph, here);
+    for (;;) {
+      const int slot = here.step % kChunkSlots;
+      const int cw = here.part % kChunkGroups;
+      const bool vals = here.part >= kChunkGroups;
+      if (here.step >= kChunkSlots &&
+          !chunk_wait(sm, vals ? &sm.v_empty[slot] : &sm.k_empty[slot],
+                      (uint32_t)(here.step / kChunkSlots - 1) & 1u))
+        break;
+      const bool zero = vs == 0.f;
+      store(vals ? sm.v[slot] : sm.k[slot], cw * 16, vals && zero);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[slot]);
-      load(p.c.k, next_ph, t, kr);
-      ks = next_ph >= 0 ? p.c.k_scale[next_ph] : 0.f;
-      vs = next_ph >= 0 ? p.c.v_scale[next_ph] : 0.f;
-      if (k_index >= kChunkSlots && !chunk_wait(sm, &sm.v_empty[slot], free_phase)) break;
-      store(sm.v[slot], vr, v_zero);
-      fence_proxy_async_smem();
+      if (lane == 0) {
+        mbar_arrive(vals ? &sm.v_full[slot] : &sm.k_full[slot]);
+        if (!vals) {  // (the softmax is never a ring of these behind)
+          const int at = here.step % kMetaSlots;
+          sm.meta[at].ks[cw] = ks;
+          sm.meta[at].lvs[cw] = ph < 0 ? -INFINITY : zero ? 0.f : log2f(vs / here.vref);
+          sm.meta[at].ivs[cw] = ph < 0 ? 0.f : zero ? 1.f : here.vref / vs;
+          mbar_arrive(&sm.meta_full[at]);
+        }
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[slot]);
       if (!more) break;
-      load(p.c.v, next_ph, t, vr);
-      ph = next_ph;
-      vref = next_vref;
+      here = there;
+      ph = page_head(here);
+      load(ph, here);
+      ks = ph >= 0 ? p.c.k_scale[ph] : 0.f;
+      vs = ph >= 0 ? p.c.v_scale[ph] : 0.f;
+      more = advance();
+      if (more) look(there);
     }
   } else if (elect_one()) {
     // ---------------- products ----------------
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         umma_f16_ts(tmem + 256u + (uint32_t)(tile * D),
                     tmem + (uint32_t)(tile * 128) + buf * 64u + (uint32_t)(8 * s),
                     b + (uint64_t)(s * 2048 >> 4), kIdPV, more || s > 0 ? 1u : 0u);
-      umma_commit(&sm.o_done[tile]);
+      umma_commit(&sm.o_done[tile][buf]);
     };
     do {
       const int n = walk.last - walk.first;
