@@ -16,6 +16,7 @@ Functions mirror the C entry points: ``pack_fp4``, ``unpack_fp4``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Dict, List, Optional, Sequence, Tuple
@@ -479,6 +480,85 @@ def sparse_attn_prefill(q, codes, scales, idx, win_k, win_v, sm_scale: Optional[
 
 
 # --- 8-bit paged key/value cache ------------------------------------------------
+#
+# These calls serve decode steps of a few microseconds, so their marshalling
+# is kept short: types and layouts are checked, the fixed parts of a cache
+# once (KV8Cache), and the current stream is read without building a Stream.
+
+_types = None
+
+
+def _kv8_types():
+    """(torch, int32, int64, bfloat16, float32, uint8), imported once."""
+    global _types
+    if _types is None:
+        torch = _torch()
+        _types = (torch, torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8)
+    return _types
+
+
+def _check_dense(t, name, dtype, dev):
+    """A contiguous CUDA tensor of this dtype on device `dev` (the current one:
+    the calls launch on its current stream)."""
+    if not isinstance(t, _types[0].Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t
+
+
+def _check_tokens(t, name, D, heads, dev):
+    """A bf16 [n, heads, D] CUDA tensor whose tokens may be strided, the heads
+    of a token dense; returns (n, heads, token stride in elements)."""
+    if not isinstance(t, _types[0].Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != _types[3]:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [n, heads, {D}]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if d != D or (heads is not None and h != heads):
+        raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {D}]")
+    if s2 != 1 or (h > 1 and s1 != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return n, h, (s0 if n > 1 else max(s0, h * D))
+
+
+def _check_step(cache, table, cu, lens, dev):
+    """table [B, width], cu [B + 1] and lens [B] of a step, and the cache's
+    device; returns (B, width)."""
+    i32 = _types[1]
+    _check_dense(table, "table", i32, dev)
+    _check_dense(cu, "cu", i32, dev)
+    _check_dense(lens, "lens", i32, dev)
+    B, width = table.shape
+    if cu.numel() != B + 1 or lens.numel() != B:
+        raise ValueError("table is [B, width], cu [B+1], lens [B]")
+    if cache.device != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
+    return B, width
+
+
+@functools.lru_cache(maxsize=256)
+def _ws_bytes(dev, query, *sizes):
+    """A workspace query's answer: it depends on the device and the sizes alone."""
+    return max(int(getattr(lib(), query)(*sizes)), 256)
+
+
+def _scratch(ws, like, dev, query, *sizes):
+    """The caller's workspace, or a new one of this call: from the caching
+    allocator, so calls on other streams and captured graphs never share it."""
+    if ws is not None:
+        return _check_dense(ws, "ws", _types[5], dev)
+    return like.new_empty(_ws_bytes(dev, query, *sizes), dtype=_types[5])
+
 
 def block_tables(lens, add, table, free_pages, block: int, cap: int, out=None):
     """Block tables and slot maps of a step: request b holds lens[b] tokens and
@@ -488,30 +568,31 @@ def block_tables(lens, add, table, free_pages, block: int, cap: int, out=None):
     [B+1], slots int64 [cap], pos int32 [cap], used int32 [1]): token offsets,
     each token's slot (page * block + row) and position (-1 past the last
     token), pages taken.  ``out``: those five tensors, to write into."""
-    torch = _torch()
-    lens = _dev(lens, "lens", torch.int32)
-    add = _dev(add, "add", torch.int32)
-    table = _dev(table, "table", torch.int32)
-    free_pages = _dev(free_pages, "free_pages", torch.int32)
+    torch, i32, i64 = _kv8_types()[:3]
+    dev = torch.cuda.current_device()
+    _check_dense(lens, "lens", i32, dev)
+    _check_dense(add, "add", i32, dev)
+    _check_dense(table, "table", i32, dev)
+    _check_dense(free_pages, "free_pages", i32, dev)
     B, width = table.shape
-    if lens.shape != (B,) or add.shape != (B,) or free_pages.dim() != 1:
-        raise ValueError("lens and add are [B], table [B, width], free_pages [n]")
+    n_free = free_pages.numel()
+    if lens.numel() != B or add.numel() != B:
+        raise ValueError("lens and add are [B], table [B, width]")
     if out is None:
-        new = lens.new_empty
-        out = (new(B), new(B + 1), new(cap, dtype=torch.int64), new(cap), new(1))
+        lens_out, cu, pos, used = lens.new_empty(2 * B + 2 + cap).split((B, B + 1, cap, 1))
+        slots = lens.new_empty(cap, dtype=i64)
+        out = (lens_out, cu, slots, pos, used)
     else:
         for t, name, n, dt in zip(out, ("lens", "cu", "slots", "pos", "used"),
-                                  (B, B + 1, cap, cap, 1),
-                                  (torch.int32, torch.int32, torch.int64, torch.int32,
-                                   torch.int32)):
-            if _dev(t, "out." + name, dt).numel() != n:
+                                  (B, B + 1, cap, cap, 1), (i32, i32, i64, i32, i32)):
+            if _check_dense(t, "out." + name, dt, dev).numel() != n:
                 raise ValueError(f"out.{name} must have {n} elements")
-    lens_out, cu, slots, pos, used = out
-    _here(lens, add, table, free_pages, *out)
-    _check(lib().csa2_block_tables(_ptr(lens), _ptr(add), B, block, _ptr(table), width,
-                                   _ptr(free_pages), free_pages.shape[0], _ptr(lens_out),
-                                   _ptr(cu), _ptr(slots), _ptr(pos), cap, _ptr(used), _stream()),
-           "csa2_block_tables")
+        lens_out, cu, slots, pos, used = out
+    rc = lib().csa2_block_tables(lens.data_ptr(), add.data_ptr(), B, block, table.data_ptr(),
+                                 width, free_pages.data_ptr(), n_free, lens_out.data_ptr(),
+                                 cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), cap,
+                                 used.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    _check(rc, "csa2_block_tables")
     return out
 
 
@@ -521,7 +602,7 @@ class KV8Cache:
     [pages, Hk, D] (contiguous CUDA tensors, kept alive by this handle)."""
 
     def __init__(self, k, v, k_scale, v_scale, k_sum):
-        torch = _torch()
+        torch = _kv8_types()[0]
         self.k, self.v = _dev(k, "k", torch.int8), _dev(v, "v", torch.int8)
         self.k_scale = _dev(k_scale, "k_scale", torch.float32)
         self.v_scale = _dev(v_scale, "v_scale", torch.float32)
@@ -534,7 +615,8 @@ class KV8Cache:
                 or k_sum.shape != (P, Hk, D)):
             raise ValueError("v must be like k, k_scale and v_scale [pages, Hk], k_sum "
                              "[pages, Hk, D]")
-        if any(x.get_device() != k.get_device() for x in (v, k_scale, v_scale, k_sum)):
+        self.device = k.get_device()
+        if any(x.get_device() != self.device for x in (v, k_scale, v_scale, k_sum)):
             raise ValueError("the tensors of a cache must be on one device")
         self._c = KV8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_sum), P, Hk,
                       self.block, D)
@@ -545,91 +627,52 @@ class KV8Cache:
         """A new cache, all zeros."""
         torch = _torch()
 
-        def zeros(shape, dtype):
+        def zeros(dtype, *shape):
             return torch.zeros(shape, dtype=dtype, device=device)
 
-        return cls(zeros((pages, Hk, block, D), torch.int8), zeros((pages, Hk, block, D),
-                                                                   torch.int8),
-                   zeros((pages, Hk), torch.float32), zeros((pages, Hk), torch.float32),
-                   zeros((pages, Hk, D), torch.int16))
-
-
-def _here(*tensors):
-    """Every tensor on the current CUDA device: the calls launch on its
-    current stream."""
-    dev = _torch().cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is "
-                             f"cuda:{dev}")
-
-
-def _scratch(nbytes, ws, device):
-    """The caller's workspace, or a new one of this call: from the caching
-    allocator, so calls on other streams and captured graphs never share it."""
-    if ws is not None:
-        return _dev(ws, "ws", _torch().uint8)
-    return _torch().empty(max(nbytes, 256), dtype=_torch().uint8, device=device)
-
-
-def _tokens(t, name, D, heads=None):
-    """A bf16 [n, heads, D] CUDA tensor whose tokens may be strided, the heads
-    of a token dense; returns its token stride in elements."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {D}]")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (t.shape[1] > 1 and s1 != D):
-        raise ValueError(f"{name}: the heads of a token must be dense")
-    return s0 if t.shape[0] > 1 else max(s0, t.shape[1] * D)
-
-
-def _step(cache, table, cu, lens):
-    torch = _torch()
-    _dev(table, "table", torch.int32)
-    _dev(cu, "cu", torch.int32)
-    _dev(lens, "lens", torch.int32)
-    B, width = table.shape
-    if cu.shape != (B + 1,) or lens.shape != (B,):
-        raise ValueError("table is [B, width], cu [B+1], lens [B]")
-    return B, width
+        return cls(zeros(torch.int8, pages, Hk, block, D), zeros(torch.int8, pages, Hk, block, D),
+                   zeros(torch.float32, pages, Hk), zeros(torch.float32, pages, Hk),
+                   zeros(torch.int16, pages, Hk, D))
 
 
 def kv8_append(cache: KV8Cache, k_new, v_new, slots):
     """Write tokens' keys and values (bf16 [n, Hk, D], tokens may be strided)
     at their slots (int64 [n], page * block + row; negative: nothing), in
     place.  The tokens of a page are consecutive, at ascending rows."""
-    ks = _tokens(k_new, "k_new", cache.D, cache.Hk)
-    vs = _tokens(v_new, "v_new", cache.D, cache.Hk)
-    _dev(slots, "slots", _torch().int64)
-    n = slots.shape[0]
-    if k_new.shape[0] != n or v_new.shape[0] != n:
+    torch, _, i64 = _kv8_types()[:3]
+    dev = torch.cuda.current_device()
+    nk, _, ks = _check_tokens(k_new, "k_new", cache.D, cache.Hk, dev)
+    nv, _, vs = _check_tokens(v_new, "v_new", cache.D, cache.Hk, dev)
+    n = _check_dense(slots, "slots", i64, dev).numel()
+    if nk != n or nv != n:
         raise ValueError("k_new, v_new and slots must have one row per token")
-    _here(cache.k, k_new, v_new, slots)
-    _check(lib().csa2_kv8_append(cache._ref, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(slots), n,
-                                 _stream()), "csa2_kv8_append")
+    if cache.device != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
+    _check(lib().csa2_kv8_append(cache._ref, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                                 slots.data_ptr(), n, torch._C._cuda_getCurrentRawStream(dev)),
+           "csa2_kv8_append")
 
 
 def kv8_unpack(cache: KV8Cache, slots, k_out=None, v_out=None):
     """The rows at slots (int64 [n]) as fp32 [n, Hk, D] keys and values (zeros
     for a negative slot)."""
-    torch = _torch()
-    _dev(slots, "slots", torch.int64)
-    shape = (slots.shape[0], cache.Hk, cache.D)
+    torch, _, i64, _, f32, _ = _kv8_types()
+    dev = torch.cuda.current_device()
+    n = _check_dense(slots, "slots", i64, dev).numel()
+    shape = (n, cache.Hk, cache.D)
+    if cache.device != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float32, device=slots.device)
+        k_out = cache.k_scale.new_empty(shape)
+    elif _check_dense(k_out, "k_out", f32, dev).shape != shape:
+        raise ValueError("k_out must be [n, Hk, D]")
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float32, device=slots.device)
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if _dev(t, name, torch.float32).shape != shape:
-            raise ValueError(f"{name} must be [n, Hk, D]")
-    _here(cache.k, slots, k_out, v_out)
-    _check(lib().csa2_kv8_unpack(cache._ref, _ptr(slots), shape[0], _ptr(k_out), _ptr(v_out),
-                                 _stream()), "csa2_kv8_unpack")
+        v_out = cache.v_scale.new_empty(shape)
+    elif _check_dense(v_out, "v_out", f32, dev).shape != shape:
+        raise ValueError("v_out must be [n, Hk, D]")
+    _check(lib().csa2_kv8_unpack(cache._ref, slots.data_ptr(), n, k_out.data_ptr(),
+                                 v_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)),
+           "csa2_kv8_unpack")
     return k_out, v_out
 
 
@@ -643,19 +686,19 @@ def kv8_select(q, cache: KV8Cache, table, cu, lens, n_sel: int, n_first: int = 1
     to: its first n_first, its last n_last and the best-scored others, int32
     [n, Hk, n_sel] ascending, then -1.  table int32 [B, width], cu int32
     [B+1] token offsets, lens int32 [B] tokens in the cache."""
-    torch = _torch()
-    stride = _tokens(q, "q", cache.D)
-    B, width = _step(cache, table, cu, lens)
-    n, H = q.shape[:2]
+    torch, i32 = _kv8_types()[:2]
+    dev = torch.cuda.current_device()
+    n, H, stride = _check_tokens(q, "q", cache.D, None, dev)
+    B, width = _check_step(cache, table, cu, lens, dev)
     if out is None:
-        out = torch.empty((n, cache.Hk, n_sel), dtype=torch.int32, device=q.device)
-    elif _dev(out, "out", torch.int32).shape != (n, cache.Hk, n_sel):
+        out = cu.new_empty((n, cache.Hk, n_sel))
+    elif _check_dense(out, "out", i32, dev).shape != (n, cache.Hk, n_sel):
         raise ValueError("out must be [n, Hk, n_sel]")
-    ws = _scratch(kv8_select_workspace_size(n, cache.Hk, width), ws, q.device)
-    _here(q, cache.k, table, cu, lens, out, ws)
-    _check(lib().csa2_kv8_select(_ptr(q), stride, cache._ref, _ptr(table), width, _ptr(cu),
-                                 _ptr(lens), B, n, H, n_sel, n_first, n_last, _ptr(out), _ptr(ws),
-                                 ws.numel(), _stream()), "csa2_kv8_select")
+    ws = _scratch(ws, cu, dev, "csa2_kv8_select_workspace_size", n, cache.Hk, width)
+    _check(lib().csa2_kv8_select(q.data_ptr(), stride, cache._ref, table.data_ptr(), width,
+                                 cu.data_ptr(), lens.data_ptr(), B, n, H, n_sel, n_first, n_last,
+                                 out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 torch._C._cuda_getCurrentRawStream(dev)), "csa2_kv8_select")
     return out
 
 
@@ -669,29 +712,31 @@ def kv8_attn(q, cache: KV8Cache, table, cu, lens, sel=None, sm_scale: Optional[f
     values already appended): q bf16 [n, H, D], table int32 [B, width], cu
     int32 [B+1], lens int32 [B]; sel int32 [n, Hk, n_sel]: only the listed
     blocks -> (out bf16 [n, H, D], lse fp32 [n, H])."""
-    torch = _torch()
-    stride = _tokens(q, "q", cache.D)
-    B, width = _step(cache, table, cu, lens)
-    n, H = q.shape[:2]
-    n_sel = 0
+    torch, i32, _, bf16, f32, _ = _kv8_types()
+    dev = torch.cuda.current_device()
+    D = cache.D
+    n, H, stride = _check_tokens(q, "q", D, None, dev)
+    B, width = _check_step(cache, table, cu, lens, dev)
+    sel_ptr, n_sel = None, 0
     if sel is not None:
-        if _dev(sel, "sel", torch.int32).dim() != 3 or sel.shape[:2] != (n, cache.Hk):
+        if _check_dense(sel, "sel", i32, dev).dim() != 3 or sel.shape[:2] != (n, cache.Hk):
             raise ValueError("sel must be [n, Hk, n_sel]")
-        n_sel = sel.shape[2]
+        sel_ptr, n_sel = sel.data_ptr(), sel.shape[2]
     if out is None:
-        out = torch.empty((n, H, cache.D), dtype=torch.bfloat16, device=q.device)
-    elif _dev(out, "out", torch.bfloat16).shape != (n, H, cache.D):
+        out = q.new_empty((n, H, D))
+    elif _check_dense(out, "out", bf16, dev).shape != (n, H, D):
         raise ValueError("out must be [n, H, D]")
     if lse is None:
-        lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
-    elif _dev(lse, "lse", torch.float32).shape != (n, H):
+        lse = cache.k_scale.new_empty((n, H))
+    elif _check_dense(lse, "lse", f32, dev).shape != (n, H):
         raise ValueError("lse must be [n, H]")
-    ws = _scratch(kv8_attn_workspace_size(n, B, H, cache.Hk, cache.D, n_sel), ws, q.device)
-    _here(q, cache.k, table, cu, lens, sel, out, lse, ws)
-    sm_scale = 1.0 / math.sqrt(cache.D) if sm_scale is None else sm_scale
-    _check(lib().csa2_kv8_attn(_ptr(q), stride, cache._ref, _ptr(table), width, _ptr(cu),
-                               _ptr(lens), B, n, H, _ptr(sel), n_sel, sm_scale, _ptr(out),
-                               _ptr(lse), _ptr(ws), ws.numel(), _stream()), "csa2_kv8_attn")
+    ws = _scratch(ws, cu, dev, "csa2_kv8_attn_workspace_size", n, B, H, cache.Hk, D, n_sel)
+    rc = lib().csa2_kv8_attn(q.data_ptr(), stride, cache._ref, table.data_ptr(), width,
+                             cu.data_ptr(), lens.data_ptr(), B, n, H, sel_ptr, n_sel,
+                             D ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(),
+                             lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                             torch._C._cuda_getCurrentRawStream(dev))
+    _check(rc, "csa2_kv8_attn")
     return out, lse
 
 

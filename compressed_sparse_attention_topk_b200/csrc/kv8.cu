@@ -294,6 +294,8 @@ csa2_status csa2_kv8_append(const csa2_kv8 *cache, const uint16_t *k_new, int64_
   p.stride[1] = v_stride;
   p.slots = slots;
   p.n = n;
+  // a decode step: a token per CTA, so that its runs go side by side; more
+  // tokens: what a page of the smallest size holds, so that few CTAs are idle
   p.group = n <= 1024 ? 1 : 16;
   TraceScope ts("kv8_append", as_stream(stream));
   return p.c.D == 64 ? launch_append_d<64>(p, as_stream(stream))

@@ -158,12 +158,14 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 // The writer.
 //
 // A run is the tokens of one page in a call: consecutive tokens at ascending
-// slots.  One CTA per (group of tokens, kv head, keys or values) looks for
-// the runs that begin in its group and, for each, keeps the run's rows in
-// registers (read once) while it takes their largest magnitude, settles the
-// page's scale, requantises the earlier rows if it grew, and writes the new
-// codes; for keys it also forms the page's code sums, so earlier rows are
-// read anyway.  Bound by bytes (4 D read + 2 D written per token and head).
+// slots.  A CTA per (group of tokens, kv head, keys or values) finds the runs
+// that begin in its group (one look at the slots for all of them) and takes
+// them in turn.  It loads the whole page at once, each row either a code row
+// from before or a new one, and keeps it in registers: largest magnitude,
+// scale, requantised old codes if the scale grew, new codes, and for keys the
+// code sums.  Bound by bytes (4 D read + 2 D written per token and head; a
+// decode step's page is mostly its earlier rows), in practice by the chain
+// slots -> rows -> scale -> codes of a run.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
 
@@ -187,47 +189,70 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   constexpr int RPP = kAppendThreads / CPR;     // rows per pass
   constexpr int PASSES = (BS + RPP - 1) / RPP;
   __shared__ float s_max[kAppendThreads / 32];
-  __shared__ int s_len;
+  __shared__ uint32_t s_runs;
+  __shared__ int s_len[2];                      // by parity of the run: one barrier less
   __shared__ int32_t s_sum[RPP][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y, vals = blockIdx.z;
+  const int h = blockIdx.y;
+  const bool vals = blockIdx.z != 0;
+  const uint16_t *x_in = vals ? p.x[1] : p.x[0];
+  const int64_t stride = vals ? p.stride[1] : p.stride[0];
   const int col = (tid % CPR) * 8, rsub = tid / CPR;
   const int64_t slots_end = (int64_t)p.c.pages * BS;
   const int64_t g0 = (int64_t)blockIdx.x * p.group;
-  const int64_t g1 = min64(g0 + p.group, p.n);
-  for (int64_t i = g0; i < g1; ++i) {
-    const int64_t slot = p.slots[i];
-    if (slot < 0) continue;
-    if (slot >= slots_end) {
-      if (tid == 0) raise_status(kStatusBadIndex);
-      continue;
+  const int count = (int)min64(p.group, p.n - g0);
+  // the tokens of the group at which a run begins (a group has at most 32)
+  if (warp == 0) {
+    bool begins = false;
+    if (lane < count) {
+      const int64_t s = p.slots[g0 + lane];
+      const int64_t before = g0 + lane > 0 ? p.slots[g0 + lane - 1] : -2;
+      if (s >= slots_end) raise_status(kStatusBadIndex);
+      begins = s >= 0 && s < slots_end && ((s & (BS - 1)) == 0 || before != s - 1);
     }
+    const uint32_t who = __ballot_sync(0xffffffffu, begins);
+    if (lane == 0) {
+      s_runs = who;
+      s_len[0] = s_len[1] = BS;
+    }
+  }
+  __syncthreads();
+  uint32_t runs = s_runs;
+  for (int turn = 0; runs; ++turn, runs &= runs - 1) {
+    const int64_t i = g0 + __ffs(runs) - 1;
+    const int64_t slot = p.slots[i];
     const int r0 = (int)(slot & (BS - 1));
-    if (i > 0 && r0 != 0 && p.slots[i - 1] == slot - 1) continue;  // inside an earlier run
-    // run length: the first row that does not follow
-    if (tid == 0) s_len = BS - r0;
-    __syncthreads();
-    if (tid < BS - r0 && (i + tid >= p.n || p.slots[i + tid] != slot + tid))
-      atomicMin(&s_len, tid);
-    __syncthreads();
-    const int m = s_len;
-    const int64_t page = slot / BS;
-    const int64_t ph = page * p.c.Hk + h;
+    const int64_t ph = slot / BS * p.c.Hk + h;
     int8_t *codes = (vals ? p.c.v : p.c.k) + ph * BS * D;
     float *scale_at = (vals ? p.c.v_scale : p.c.k_scale) + ph;
     const float s_old = r0 ? *scale_at : 0.f;
-    const uint16_t *src = p.x[vals] + i * p.stride[vals] + (int64_t)h * D + col;
-
+    // the run's length: the first row whose token does not follow
+    if (tid < BS - r0 && (i + tid >= p.n || p.slots[i + tid] != slot + tid))
+      atomicMin(&s_len[turn & 1], tid);
+    // the page's rows: 8 codes (x, y) before r0, 8 new values from there
     uint4 x[PASSES];
-    float big = 0.f;
 #pragma unroll
     for (int a = 0; a < PASSES; ++a) {
       const int r = a * RPP + rsub;
       x[a] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < m) x[a] = *reinterpret_cast<const uint4 *>(src + r * p.stride[vals]);
+      if (r < r0) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(codes + r * D + col);
+        x[a].x = w.x;
+        x[a].y = w.y;
+      }
     }
+    __syncthreads();
+    const int end = min(r0 + s_len[turn & 1], BS);
+    const uint16_t *src = x_in + (i - r0) * stride + (int64_t)h * D + col;
 #pragma unroll
     for (int a = 0; a < PASSES; ++a) {
+      const int r = a * RPP + rsub;
+      if (r >= r0 && r < end) x[a] = *reinterpret_cast<const uint4 *>(src + r * stride);
+    }
+    float big = 0.f;
+#pragma unroll
+    for (int a = 0; a < PASSES; ++a) {
+      if (a * RPP + rsub < r0) continue;
       const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -237,47 +262,39 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     }
     big = warp_max(big);
     if (lane == 0) s_max[warp] = big;
-    __syncthreads();  // (also: every thread has read the old scale)
+    __syncthreads();  // (also: every thread has read the old scale and the length)
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) big = fmaxf(big, s_max[w]);
     const float s = fmaxf(s_old, __fdiv_rn(big, 127.f));
-    if (tid == 0) *scale_at = s;
-
-    int32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const bool grew = s > s_old;
-    if (grew || !vals) {  // earlier rows: requantised, and summed for the keys
-      const float ratio = grew ? __fdiv_rn(s_old, s) : 1.f;
-      for (int r = rsub; r < r0; r += RPP) {
-        uint2 *at = reinterpret_cast<uint2 *>(codes + r * D + col);
-        const uint2 w = *at;
-        uint32_t o[2] = {w.x, w.y};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          int c = (int8_t)(o[e >> 2] >> (8 * (e & 3)));
-          if (grew) {
-            c = __float2int_rn(__fmul_rn((float)c, ratio));
-            o[e >> 2] = (o[e >> 2] & ~(0xffu << (8 * (e & 3)))) |
-                        ((uint32_t)(uint8_t)c << (8 * (e & 3)));
-          }
-          sum[e] += c;
-        }
-        if (grew) *at = make_uint2(o[0], o[1]);
-      }
+    const float ratio = grew ? __fdiv_rn(s_old, s) : 1.f;
+    if (tid == 0) {
+      *scale_at = s;
+      s_len[(turn & 1) ^ 1] = BS;
     }
+    int32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int a = 0; a < PASSES; ++a) {
       const int r = a * RPP + rsub;
-      if (r >= m) continue;
+      if (r >= end) continue;
+      const bool old = r < r0;
       const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
       uint32_t o[2] = {0u, 0u};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t bits = (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16);
-        const int c = s > 0.f ? kv8_code(__uint_as_float(bits), s) : 0;
+        int c;
+        if (old) {
+          c = (int8_t)(w[e >> 2] >> (8 * (e & 3)));
+          if (grew) c = __float2int_rn(__fmul_rn((float)c, ratio));
+        } else {
+          const uint32_t bits = (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16);
+          c = s > 0.f ? kv8_code(__uint_as_float(bits), s) : 0;
+        }
         o[e >> 2] |= (uint32_t)(uint8_t)c << (8 * (e & 3));
         sum[e] += c;
       }
-      *reinterpret_cast<uint2 *>(codes + (r0 + r) * D + col) = make_uint2(o[0], o[1]);
+      if (!old || grew)
+        *reinterpret_cast<uint2 *>(codes + r * D + col) = make_uint2(o[0], o[1]);
     }
     if (!vals) {
 #pragma unroll
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
         p.c.k_sum[ph * D + tid] = (int16_t)t;
       }
     }
-    __syncthreads();  // s_len, s_max and s_sum are free again
+    __syncthreads();  // s_max, s_sum and s_len are free again
   }
 }
 

@@ -142,9 +142,13 @@ def test_workspace_queries(lib):
 
 def test_bindings_refuse_host_tensors():
     x = torch.zeros(2, dtype=torch.int32)
+    csa2._kv8_types()
     with pytest.raises(TypeError):
-        csa2.block_tables(x, x, torch.zeros(2, 4, dtype=torch.int32), x, 64, 8)
+        csa2._check_dense(x, "x", torch.int32, 0)
     with pytest.raises(TypeError):
         csa2.KV8Cache(*[torch.zeros(1)] * 5)
     with pytest.raises(TypeError):
-        csa2._tokens(torch.zeros(2, 4, 64, dtype=torch.bfloat16), "q", 64)
+        csa2._check_tokens(torch.zeros(2, 4, 64, dtype=torch.bfloat16), "q", 64, None, 0)
+    if torch.cuda.is_available():
+        with pytest.raises(TypeError):
+            csa2.block_tables(x, x, torch.zeros(2, 4, dtype=torch.int32), x, 64, 8)
