@@ -8,9 +8,11 @@
 // in fp16, and so is q once its row is scaled by a power of two (its largest
 // magnitude goes to [1, 2); what is more than 2^-14 below it loses bits that
 // weigh less than fp32's in the dot), so the products are exact and their
-// sums fp32.  The weights are rounded once to fp16 as 2^14 p: 2^-11 of each
-// weight, and weights down to 2^-38 are not lost.  Sums of weights, maxima
-// and outputs stay in fp32; a page's scale multiplies its fp32 partial
+// sums fp32.  m follows the running maximum only when that has grown by more
+// than kSlack, which one vote of the warp finds out; so a row's maximum is
+// seldom reduced and its output seldom rescaled.  The weights are rounded once
+// to fp16, 2^10 at m: 2^-11 of each weight, and weights down to 2^-34 of the
+// largest are not lost.  Sums of weights and outputs stay in fp32; a page's scale multiplies its fp32 partial
 // output, so scales far apart lose nothing.
 #pragma once
 
@@ -132,7 +134,7 @@ constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = 32 * kSplitWarps;
 constexpr int kUnit = 32;
 constexpr int kNoPos = 1 << 30;  // a table reaches fewer positions; no row sees this one
-constexpr float kPBias = 14.f;  // weights are held as 2^14 p
+constexpr float kPBias = 10.f, kSlack = 5.f;  // weights are at most 2^(10 + 5) < 65504
 
 template <int D, int R8>
 struct SplitShape {
@@ -229,6 +231,18 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
   const long long c = blockIdx.x;
   u0 = c < ctas ? W * c / ctas : W;
   u1 = c < ctas ? W * (c + 1) / ctas : W;
+  if (p.sel && W > 0 && W / list_units * 2 <= gridDim.x) {
+    // few lists, all as long: the same number of CTAs for each, so that none
+    // works on two
+    const long long lists = W / list_units;
+    const long long each = min((long long)gridDim.x / lists,
+                               max(1ll, (long long)list_units / kSplitWarps));
+    u0 = u1 = W;
+    if (c < lists * each) {
+      u0 = c / each * list_units + list_units * (c % each) / each;
+      u1 = c / each * list_units + list_units * (c % each + 1) / each;
+    }
+  }
   if (u0 >= u1) {
     if (tid == 0) p.rec[c] = make_int4(-1, 0, 0, 0);
     return;
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       const long long th = idx / xt;
       const int64_t tok = th / p.c.Hk;
       tl.h = (int)(th - tok * p.c.Hk);
-      tl.b = max(seq_of(p.s, tok), 0);
+      tl.b = max(seq_of(p.s, tok, lane), 0);
       tl.tok0 = (int)tok;
       tl.pos0 = (int)max((int64_t)-0x40000000,
                          (int64_t)p.s.lens[tl.b] - p.s.cu[tl.b + 1] + tok);
@@ -358,15 +372,16 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       }
     }
 
-    // ---- state: weights are 2^(x - z) ----
-    float o[R8][DT][4], m[R8][2], z[R8][2], l[R8][2];
+    // ---- state: weights are 2^(x - z); one above 2^lim moves z (any does
+    // where z is not set yet) ----
+    float o[R8][DT][4], lim[R8][2], z[R8][2], l[R8][2];
 #pragma unroll
     for (int q8 = 0; q8 < R8; ++q8) {
 #pragma unroll
       for (int j = 0; j < DT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[q8][j][e] = 0.f;
-      m[q8][0] = m[q8][1] = -INFINITY;
+      lim[q8][0] = lim[q8][1] = -INFINITY;
       z[q8][0] = z[q8][1] = 0.f;
       l[q8][0] = l[q8][1] = 0.f;
     }
@@ -505,7 +520,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[q8][k][e] *= fac[q8][e & 1] * ks[k];
+            for (int e = 0; e < 4; ++e)
+              sc[q8][k][e] = fmaf(sc[q8][k][e], fac[q8][e & 1] * ks[k], -z[q8][e & 1]);
         if (max(pos[0], pos[1]) + 15 > tl.pos_first) {  // not seen whole by every row
 #pragma unroll
           for (int q8 = 0; q8 < R8; ++q8)
@@ -515,47 +531,59 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
               for (int e = 0; e < 4; ++e)
                 if (pos[k] + g + (e >> 1) * 8 > row_pos[q8][e & 1]) sc[q8][k][e] = -INFINITY;
         }
-        uint32_t pb[R8][2][2];
-        float corr[R8][2];
-        bool moved = false;
+        float top[R8][2];
+        bool move = false;
 #pragma unroll
-        for (int q8 = 0; q8 < R8; ++q8) {
+        for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(sc[q8][0][e], sc[q8][0][e + 2]),
-                             fmaxf(sc[q8][1][e], sc[q8][1][e + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float old = m[q8][e];
-            mx = fmaxf(mx, old);
-            const float zero = (mx == -INFINITY ? 0.f : mx) - kPBias;
-            corr[q8][e] = old == mx ? 1.f : old == -INFINITY ? 0.f : ex2(z[q8][e] - zero);
-            moved |= old != mx;
-            m[q8][e] = mx;
-            z[q8][e] = zero;
-            float sum = 0.f;
+            top[q8][e] = fmaxf(fmaxf(sc[q8][0][e], sc[q8][0][e + 2]),
+                               fmaxf(sc[q8][1][e], sc[q8][1][e + 2]));
+            move |= top[q8][e] > lim[q8][e];
+          }
+        if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              sc[q8][k][e] = ex2(sc[q8][k][e] - zero);
-              sc[q8][k][e + 2] = ex2(sc[q8][k][e + 2] - zero);
-              sum += sc[q8][k][e] + sc[q8][k][e + 2];
+          for (int q8 = 0; q8 < R8; ++q8) {
+            float corr[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = top[q8][e];
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              corr[e] = 1.f;
+              if (mx > lim[q8][e]) {
+                const float to = z[q8][e] + (mx - kPBias), by = to - z[q8][e];
+                if (lim[q8][e] > 0.f) corr[e] = ex2(-by);  // (else there are no weights yet)
+                z[q8][e] = to;
+                lim[q8][e] = kPBias + kSlack;
+                l[q8][e] *= corr[e];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  sc[q8][k][e] -= by;
+                  sc[q8][k][e + 2] -= by;
+                }
+              }
             }
-            l[q8][e] = l[q8][e] * corr[q8][e] + sum;
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            pb[q8][k][0] = transpose_8x8(pack_f16(sc[q8][k][0], sc[q8][k][1]));
-            pb[q8][k][1] = transpose_8x8(pack_f16(sc[q8][k][2], sc[q8][k][3]));
-          }
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-          for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
             for (int j = 0; j < DT; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[q8][j][e] *= corr[q8][e & 1];
+              for (int e = 0; e < 4; ++e) o[q8][j][e] *= corr[e & 1];
+          }
+        }
+        uint32_t pb[R8][2][2];
+#pragma unroll
+        for (int q8 = 0; q8 < R8; ++q8) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[q8][k][e] = ex2(sc[q8][k][e]);
+            pb[q8][k][0] = transpose_8x8(pack_f16(sc[q8][k][0], sc[q8][k][1]));
+            pb[q8][k][1] = transpose_8x8(pack_f16(sc[q8][k][2], sc[q8][k][3]));
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            l[q8][e] += (sc[q8][0][e] + sc[q8][0][e + 2]) + (sc[q8][1][e] + sc[q8][1][e + 2]);
         }
         // ---- O^T += vs * V^T P^T: rows g and g + 8 of 16-dim tile j are
         // dims g DT 2 + j and + DT + j, so a thread's bytes of a token are

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 // slots -> rows -> scale -> codes of a run.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
+constexpr int kAppendGroup = 32;  // tokens per CTA at most
 
 struct AppendParams {
   Cache c;
@@ -178,9 +179,8 @@ struct AppendParams {
   int32_t group;  // tokens per CTA
 };
 
-__device__ __forceinline__ int8_t kv8_code(float x, float s) {
-  const int q = __float2int_rn(__fdiv_rn(x, s));
-  return (int8_t)max(-127, min(127, q));
+__device__ __forceinline__ int kv8_code(float x, float s) {
+  return max(-127, min(127, __float2int_rn(__fdiv_rn(x, s))));
 }
 
 template <int D, int BS>
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   constexpr int RPP = kAppendThreads / CPR;     // rows per pass
   constexpr int PASSES = (BS + RPP - 1) / RPP;
   __shared__ float s_max[kAppendThreads / 32];
+  __shared__ int64_t s_slot[kAppendGroup + BS];  // of tokens g0 - 1 ..
   __shared__ uint32_t s_runs;
   __shared__ int s_len[2];                      // by parity of the run: one barrier less
   __shared__ int32_t s_sum[RPP][D];
@@ -201,14 +202,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   const int64_t slots_end = (int64_t)p.c.pages * BS;
   const int64_t g0 = (int64_t)blockIdx.x * p.group;
   const int count = (int)min64(p.group, p.n - g0);
-  // the tokens of the group at which a run begins (a group has at most 32)
+  // the group's slots, the one before them and what its last run may reach
+  for (int k = tid; k < kAppendGroup + BS; k += kAppendThreads) {
+    const int64_t at = g0 + k - 1;
+    s_slot[k] = at >= 0 && at < p.n ? p.slots[at] : -2;
+  }
+  __syncthreads();
+  // the tokens of the group at which a run begins
   if (warp == 0) {
     bool begins = false;
     if (lane < count) {
-      const int64_t s = p.slots[g0 + lane];
-      const int64_t before = g0 + lane > 0 ? p.slots[g0 + lane - 1] : -2;
+      const int64_t s = s_slot[lane + 1];
       if (s >= slots_end) raise_status(kStatusBadIndex);
-      begins = s >= 0 && s < slots_end && ((s & (BS - 1)) == 0 || before != s - 1);
+      begins = s >= 0 && s < slots_end && ((s & (BS - 1)) == 0 || s_slot[lane] != s - 1);
     }
     const uint32_t who = __ballot_sync(0xffffffffu, begins);
     if (lane == 0) {
@@ -219,15 +225,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
   __syncthreads();
   uint32_t runs = s_runs;
   for (int turn = 0; runs; ++turn, runs &= runs - 1) {
-    const int64_t i = g0 + __ffs(runs) - 1;
-    const int64_t slot = p.slots[i];
+    const int in_group = __ffs(runs) - 1;
+    const int64_t i = g0 + in_group;
+    const int64_t slot = s_slot[in_group + 1];
     const int r0 = (int)(slot & (BS - 1));
     const int64_t ph = slot / BS * p.c.Hk + h;
     int8_t *codes = (vals ? p.c.v : p.c.k) + ph * BS * D;
     float *scale_at = (vals ? p.c.v_scale : p.c.k_scale) + ph;
     const float s_old = r0 ? *scale_at : 0.f;
     // the run's length: the first row whose token does not follow
-    if (tid < BS - r0 && (i + tid >= p.n || p.slots[i + tid] != slot + tid))
+    if (tid < BS - r0 && s_slot[in_group + 1 + tid] != slot + tid)
       atomicMin(&s_len[turn & 1], tid);
     // the page's rows: 8 codes (x, y) before r0, 8 new values from there
     uint4 x[PASSES];
@@ -364,16 +371,19 @@ struct Steps {
   int64_t n;
 };
 
-// The sequence that owns token i (cu[b] <= i < cu[b+1]), or -1 for padding.
-__device__ __forceinline__ int seq_of(const Steps &s, int64_t i) {
-  if (s.B == 0 || i >= s.cu[s.B]) return -1;
-  int lo = 0, hi = s.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s.cu[mid] <= i) lo = mid;
-    else hi = mid;
+// The sequence that owns token i (cu[b] <= i < cu[b+1]), or -1 for padding: a
+// whole warp looks at 32 offsets a round.
+__device__ __forceinline__ int seq_of(const Steps &s, int64_t i, int lane) {
+  const int32_t total = s.cu[s.B];
+  int lo = 0, n = s.B;  // cu[lo] <= i, and the owner is among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const uint32_t who = __ballot_sync(0xffffffffu, lane * step < n && s.cu[at] <= i);
+    const int k = who ? 31 - __clz(who) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  return lo;
+  return i < total ? lo : -1;
 }
 
 }  // namespace kv8

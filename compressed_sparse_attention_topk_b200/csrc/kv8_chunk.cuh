@@ -17,7 +17,7 @@
 //   y_j = x_j + log2(vs / vref),  P_j = 2^(y_j - m),  m >= max y - kSlack,
 // so P_j vcode_j vref is p_j vs vcode_j in the row's own units, whatever the
 // scales; the softmax sum takes P_j (vref / vs) page by page.  P is rounded
-// once to fp16, 2^kChunkBias at m: 2^-11 of a weight, down to 2^-34 of the
+// once to fp16, 2^kPBias at m: 2^-11 of a weight, down to 2^-34 of the
 // largest.  m follows the running maximum only when that has grown by more
 // than kSlack, so O is rarely rescaled.
 //
@@ -40,7 +40,6 @@ constexpr int kChunkRows = 256;
 constexpr int kSoftWarps = 8;
 constexpr int kConvWarps = 7;  // with the products' 16 warps: 128 registers a thread
 constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + 1);
-constexpr float kChunkBias = 10.f, kSlack = 5.f;  // 2^(10 + 5) < 65504
 constexpr int kMetaSlots = 8;
 
 template <int D>
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
           }
         }
         // ---- weights over S, sums ----
-        const float zero = (m == -INFINITY ? 0.f : m) - kChunkBias;
+        const float zero = (m == -INFINITY ? 0.f : m) - kPBias;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t w[16];
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const float vref = chunk_vref(p, walk.b, walk.h);
       const bool mine_out = r < walk.nrows;
       const int64_t at = (int64_t)(walk.s.t0 + tok) * (p.G * p.c.Hk) + head;
-      const float zero = m - kChunkBias;
+      const float zero = m - kPBias;
       float *part = p.part + (2 * c + (walk.first > 0 ? 0 : 1)) * S::PART;
       const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref;
 #pragma unroll 1

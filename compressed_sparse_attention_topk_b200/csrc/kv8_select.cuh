@@ -12,7 +12,7 @@
 // for a chunk.  kv8_pick_*_kernel then takes each row's n_sel best: a score is
 // ordered as an unsigned key, forced blocks get the largest key, and the
 // n_sel-th largest key is found by bisection within a warp (rows of up to
-// 2,048 blocks, keys in registers) or by digits over a CTA.  Both latency-bound.
+// 2,048 blocks) or by digits over a CTA.  Both latency-bound.
 #pragma once
 
 #include "kv8_cache.cuh"
@@ -60,7 +60,7 @@ __device__ __forceinline__ int seen_blocks(int64_t pos, int shift, int width) {
 // one sequence: with f(b) = cu[b] / (8 R) + b, tiles f(b) .. f(b + 1) - 1
 // belong to sequence b (enough for its tokens; a last one may be empty).
 template <int D, int R>
-__global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 2) kv8_score_kernel(const SelectParams p) {
   constexpr int TT = 8 * R;
   constexpr int KS = D / 32;       // k-steps
   constexpr int LD = D + 32;       // bytes per token of q8: its reads meet no bank twice
@@ -183,26 +183,32 @@ __global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const SelectPa
 
   // ---- 16 blocks at a time ----
   for (; gi < groups; gi += stride) {
-    int32_t hi[R][4], lo[R][4];
+    int32_t acc[R][4];  // 256 times the high bytes' dots, then the low bytes' on top
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hi[r][e] = lo[r][e] = 0;
+      for (int e = 0; e < 4; ++e) acc[r][e] = 0;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      // bytes of dims 0..3 (first word) and 4..7 of the thread's 8
-      const uint32_t al[4] = {__byte_perm(x[0][s].x, x[0][s].y, 0x6420),
-                              __byte_perm(x[1][s].x, x[1][s].y, 0x6420),
-                              __byte_perm(x[0][s].z, x[0][s].w, 0x6420),
-                              __byte_perm(x[1][s].z, x[1][s].w, 0x6420)};
-      const uint32_t ah[4] = {__byte_perm(x[0][s].x, x[0][s].y, 0x7531),
-                              __byte_perm(x[1][s].x, x[1][s].y, 0x7531),
-                              __byte_perm(x[0][s].z, x[0][s].w, 0x7531),
-                              __byte_perm(x[1][s].z, x[1][s].w, 0x7531)};
+    for (int low = 0; low < 2; ++low) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        mma_i8<true>(lo[r], al, qb[r][s][0], qb[r][s][1]);
-        mma_i8<false>(hi[r], ah, qb[r][s][0], qb[r][s][1]);
+      for (int s = 0; s < KS; ++s) {
+        // bytes of dims 0..3 (first word) and 4..7 of the thread's 8
+        const uint32_t pick = low ? 0x6420u : 0x7531u;
+        const uint32_t a[4] = {__byte_perm(x[0][s].x, x[0][s].y, pick),
+                               __byte_perm(x[1][s].x, x[1][s].y, pick),
+                               __byte_perm(x[0][s].z, x[0][s].w, pick),
+                               __byte_perm(x[1][s].z, x[1][s].w, pick)};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (low) mma_i8<true>(acc[r], a, qb[r][s][0], qb[r][s][1]);
+          else mma_i8<false>(acc[r], a, qb[r][s][0], qb[r][s][1]);
+        }
+      }
+      if (!low) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][e] *= 256;
       }
     }
     const int j0 = gi * 16 + g;
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const SelectPa
       for (int e = 0; e < 4; ++e) {
         const int i = r * 8 + 2 * t + (e & 1), j = j0 + (e >> 1) * 8;
         if (i < count && j < nblk) {
-          const float dot = (float)(hi[r][e] * 256 + lo[r][e]);
+          const float dot = (float)acc[r][e];
           const float sc = __fadd_rn(__fmul_rn(dot, (e >> 1) ? k1 : k0), 0.f);
           p.scores[((tok0 + i) * p.c.Hk + h) * p.s.width + j] =
               ((e >> 1) ? bad1 : bad0) ? -INFINITY : sc;
@@ -239,70 +245,92 @@ __device__ __forceinline__ uint32_t pick_key(const SelectParams &p, const float 
   return max(score_key(row[j]), 1u);
 }
 
-// One warp per row of up to 32 K blocks; lane l holds blocks 32 i + l.
+// One warp per row of up to 32 K blocks.  Where at most 32 are wanted the
+// smallest of the lanes' largest keys is a bound that at least 32 keys reach:
+// only those keys (some 130 of 1,024 in a random order) are listed, in block
+// order, and searched.
+constexpr int kPickWarps = 4;
+
 template <int K>
-__global__ void __launch_bounds__(128) kv8_pick_warp_kernel(const SelectParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(32 * kPickWarps) kv8_pick_warp_kernel(const SelectParams p) {
+  __shared__ uint32_t s_key[kPickWarps][32 * K];
+  __shared__ uint16_t s_block[kPickWarps][32 * K];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t item = (int64_t)blockIdx.x * kPickWarps + warp;
   const int64_t i = item / p.c.Hk;
   if (i >= p.s.n) return;
-  const int b = seq_of(p.s, i);
+  const int b = seq_of(p.s, i, lane);
   if (b < 0) return;
   const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
   const int nblk = seen_blocks(pos, p.c.bs_shift, p.s.width);
-  pdl_wait_primary();
-  const float *row = p.scores + item * p.s.width;
   int32_t *out = p.sel + item * p.n_sel;
-  const int want = min(p.n_sel, nblk);
+  const int first = min(p.n_first, nblk), last = max(first, nblk - p.n_last);
+  const int want = min(p.n_sel - (first + nblk - last), last - first);
+  pdl_wait_primary();
+  if (want == last - first) {  // all of them
+    for (int o = lane; o < p.n_sel; o += 32) out[o] = o < nblk ? o : -1;
+    return;
+  }
+  const float *row = p.scores + item * p.s.width;
   uint32_t key[K];
   uint32_t top = 0u;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    key[k] = pick_key(p, row, k * 32 + lane, nblk);
+    const int j = k * 32 + lane;
+    key[k] = j >= first && j < last ? max(score_key(row[j]), 1u) : 0u;
     top = max(top, key[k]);
   }
-  // lo: at least `want` keys reach it; hi: fewer do.  Up to 32 wanted, the
-  // smallest of the lanes' largest keys is such a lo.
+  // lo: at least `want` keys reach it; hi: fewer do
   uint32_t lo = want <= 32 ? max(__reduce_min_sync(0xffffffffu, top), 1u) : 1u;
   uint64_t hi = (uint64_t)__reduce_max_sync(0xffffffffu, top) + 1;
-  uint32_t above = 0u;  // keys that reach hi
-  bool ties = true;
-  while (hi - lo > 1) {
-    const uint32_t mid = (uint32_t)((lo + hi) >> 1);
-    uint32_t n = 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) n += key[k] >= mid ? 1u : 0u;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (n >= (uint32_t)want) {
-      lo = mid;
-      if (n == (uint32_t)want) {
-        ties = false;
-        break;
-      }
-    } else {
-      hi = mid;
-      above = n;
-    }
-  }
-  // kept, in ascending order: keys that reach lo, of those that equal it the
-  // lowest blocks only
-  uint32_t left = ties ? (uint32_t)want - above : 0xffffffffu;
-  int at = 0;
+  uint32_t *keys = s_key[warp];
+  uint16_t *blocks = s_block[warp];
   const uint32_t lt = lanemask_lt_u32();
+  int n = 0;  // listed
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    bool keep = key[k] >= lo;
+    const bool in = key[k] >= lo;
+    const uint32_t who = __ballot_sync(0xffffffffu, in);
+    if (in) {
+      const int at = n + __popc(who & lt);
+      keys[at] = key[k];
+      blocks[at] = (uint16_t)(k * 32 + lane);
+    }
+    n += __popc(who);
+  }
+  __syncwarp();
+  uint32_t above = 0u;  // keys that reach hi
+  bool ties = n != want;
+  while (ties && hi - lo > 1) {
+    const uint32_t mid = (uint32_t)((lo + hi) >> 1);
+    uint32_t reach = 0;
+    for (int x = lane; x < n; x += 32) reach += keys[x] >= mid ? 1u : 0u;
+    reach = __reduce_add_sync(0xffffffffu, reach);
+    if (reach >= (uint32_t)want) {
+      lo = mid;
+      ties = reach != (uint32_t)want;
+    } else {
+      hi = mid;
+      above = reach;
+    }
+  }
+  // kept: keys that reach lo, of those that equal it the lowest blocks only
+  uint32_t left = ties ? (uint32_t)want - above : 0xffffffffu;
+  int at = first;
+  for (int x0 = 0; x0 < n; x0 += 32) {
+    const uint32_t k = x0 + lane < n ? keys[x0 + lane] : 0u;
+    bool keep = k >= lo;
     if (ties) {
-      const bool eq = key[k] == lo;
-      const uint32_t who = __ballot_sync(0xffffffffu, eq);
-      if (eq) keep = (uint32_t)__popc(who & lt) < left;
+      const uint32_t who = __ballot_sync(0xffffffffu, k == lo);
+      if (k == lo) keep = (uint32_t)__popc(who & lt) < left;
       left -= min(left, (uint32_t)__popc(who));
     }
     const uint32_t kept = __ballot_sync(0xffffffffu, keep);
-    if (keep) out[at + __popc(kept & lt)] = k * 32 + lane;
+    if (keep) out[at + __popc(kept & lt)] = blocks[x0 + lane];
     at += __popc(kept);
   }
-  for (int o = at + lane; o < p.n_sel; o += 32) out[o] = -1;
+  for (int o = lane; o < first; o += 32) out[o] = o;
+  for (int o = lane; o < nblk - last; o += 32) out[at + o] = last + o;
 }
 
 // One CTA per row: the threshold by three digits (11, 11 and 10 bits), each
@@ -316,7 +344,7 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_cta_kernel(const Select
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t item = blockIdx.x;
   const int64_t i = item / p.c.Hk;
-  const int b = seq_of(p.s, i);
+  const int b = seq_of(p.s, i, lane);
   if (b < 0) return;
   const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
   const int nblk = seen_blocks(pos, p.c.bs_shift, p.s.width);
