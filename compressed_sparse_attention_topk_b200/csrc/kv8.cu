@@ -178,7 +178,7 @@ AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
 template <int D, int ROWS>
 csa2_status launch_merge(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
   TraceScope ts("kv8_attn_merge", st);
-  return launch_dependent(kv8::kv8_merge_kernel<D, ROWS>, dim3((unsigned)a.ctas, ROWS / 4),
+  return launch_dependent(kv8::kv8_merge_kernel<D, ROWS>, dim3((unsigned)a.ctas, ROWS / kv8::merge_rows(ROWS)),
                           kv8::kMergeThreads, 0, st, p, a.ctas);
 }
 

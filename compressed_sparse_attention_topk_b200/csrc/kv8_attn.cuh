@@ -727,22 +727,26 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 
 // ---------------------------------------------------------------------------
 // Tiles of ROWS query rows that several CTAs shared (of kv8_split_kernel, or
-// of kv8_chunk_kernel): block (c, y) merges
-// rows 4 y .. 4 y + 3 of the tile that CTA c begins and later CTAs end, in
-// CTA order.  Two warps per row, eight partials in flight each.
+// of kv8_chunk_kernel): block (c, y) merges rows RPB y .. of the tile that CTA
+// c begins and later CTAs end, in CTA order.  WPR warps share a row's
+// partials, eight in flight each: two for a few rows with many partials, one
+// for a chunk's 256 rows with few.
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
+constexpr int merge_rows(int rows) { return rows > 32 ? 32 : 4; }  // per block
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int ctas) {
   constexpr size_t PART = size_t(ROWS) * (D + 2);
+  constexpr int RPB = ROWS > 32 ? 32 : 4;
+  constexpr int WPR = RPB == 4 ? 2 : 1;
   constexpr int E = D / 32;
   __shared__ float s_o[8][D], s_ml[8][2];
   const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait_primary();
   const int4 rec = p.rec[c];
   const int nrows = rec.y >> 8;
-  if (rec.x < 0 || (int)blockIdx.y * 4 >= nrows) return;
+  if (rec.x < 0 || (int)blockIdx.y * RPB >= nrows) return;
   // the tile's partials: (c, 1), (c + 1, 0), ..., up to the CTA that ends it
   int end = c + 1;
   for (; end < ctas; end += 32) {
@@ -754,48 +758,57 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
     }
   }
   const int count = min(end, ctas - 1) - c + 1;
-  const int r = blockIdx.y * 4 + (warp >> 1);
-  const int half = (count + 1) / 2;
-  const int k0 = (warp & 1) * half, k1 = min(count, k0 + half);
-  float m = -INFINITY, l = 0.f, o[E];
+  const int half = (count + WPR - 1) / WPR;
+  const int k0 = (warp % WPR) * half, k1 = min(count, k0 + half);
+  auto at = [&](int k) { return p.part + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * PART; };
+#pragma unroll 1
+  for (int r = blockIdx.y * RPB + warp / WPR; r < (int)(blockIdx.y + 1) * RPB; r += 8 / WPR) {
+    float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (r < nrows) {
-    auto at = [&](int k) { return p.part + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * PART; };
-    for (int k = k0 + lane; k < k1; k += 32) m = fmaxf(m, at(k)[ROWS * D + r]);
-    m = warp_max(m);
-    const float zero = m == -INFINITY ? 0.f : m;
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    if (r < nrows) {
+      for (int k = k0 + lane; k < k1; k += 32) m = fmaxf(m, at(k)[ROWS * D + r]);
+      m = warp_max(m);
+      const float zero = m == -INFINITY ? 0.f : m;
 #pragma unroll 8
-    for (int k = k0; k < k1; ++k) {
-      const float *src = at(k);
-      const float f = ex2(src[ROWS * D + r] - zero);
-      l = fmaf(src[ROWS * D + ROWS + r], f, l);
+      for (int k = k0; k < k1; ++k) {
+        const float *src = at(k);
+        const float f = ex2(src[ROWS * D + r] - zero);
+        l = fmaf(src[ROWS * D + ROWS + r], f, l);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(src[r * D + lane * E + e], f, o[e]);
+        for (int e = 0; e < E; ++e) o[e] = fmaf(src[r * D + lane * E + e], f, o[e]);
+      }
     }
-  }
+    float sum = l, zero = m == -INFINITY ? 0.f : m;
+    if constexpr (WPR == 2) {  // (one row per pair of warps: no second turn)
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    s_ml[warp][0] = m;
-    s_ml[warp][1] = l;
-  }
-  __syncthreads();
-  if ((warp & 1) || r >= nrows) return;
-  const float m1 = s_ml[warp + 1][0], mx = fmaxf(m, m1), zero = mx == -INFINITY ? 0.f : mx;
-  const float f0 = ex2(m - zero), f1 = ex2(m1 - zero);
-  const float sum = l * f0 + s_ml[warp + 1][1] * f1;
-  const int R = rec.w + r, tok = R / p.G;
-  const int64_t row = (int64_t)(rec.x + tok) * (p.G * p.c.Hk) + (rec.y & 255) * p.G + R - tok * p.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+      if (lane == 0) {
+        s_ml[warp][0] = m;
+        s_ml[warp][1] = l;
+      }
+      __syncthreads();
+      if (warp & 1) return;
+      const float m1 = s_ml[warp + 1][0], mx = fmaxf(m, m1);
+      zero = mx == -INFINITY ? 0.f : mx;
+      const float f0 = ex2(m - zero);
+      const float f1 = ex2(m1 - zero);
+      sum = l * f0 + s_ml[warp + 1][1] * f1;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float y = (o[e] * f0 + s_o[warp + 1][lane * E + e] * f1) * inv;
-    p.out[row * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16(y));
+      for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + s_o[warp + 1][lane * E + e] * f1;
+    }
+    if (r >= nrows) continue;
+    const int R = rec.w + r, tok = R / p.G;
+    const int64_t row =
+        (int64_t)(rec.x + tok) * (p.G * p.c.Hk) + (rec.y & 255) * p.G + R - tok * p.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      p.out[row * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16(o[e] * inv));
+    if (lane == 0 && p.lse)
+      p.lse[row] =
+          sum == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(sum));
   }
-  if (lane == 0 && p.lse)
-    p.lse[row] =
-        sum == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(sum));
 }
 
 }  // namespace kv8

@@ -759,31 +759,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const int n = walk.last - walk.first;
       const int tiles = walk.nrows > 128 ? 2 : 1;
       for (int i = 0; i < tiles && ok; ++i) ok = chunk_wait(sm, &sm.q_full[i], n_seg[i]++ & 1u);
-      for (int t = -1; t < n && ok; ++t) {
-        // the next step's logits before this one's weights are waited for
-        const int slot = k_index % kChunkSlots, next_slot = (k_index + 1) % kChunkSlots;
-        const bool next = t + 1 < n;
-        const int k_slot = t < 0 ? slot : next_slot, k_at = t < 0 ? k_index : k_index + 1;
-        if (next && !(ok = chunk_wait(sm, &sm.k_full[k_slot], (uint32_t)(k_at / kChunkSlots) & 1u)))
-          break;
-        if (t >= 0 &&
-            !(ok = chunk_wait(sm, &sm.v_full[slot], (uint32_t)(k_index / kChunkSlots) & 1u)))
-          break;
-        tc_fence_after();
-        for (int i = 0; i < tiles; ++i) {
-          if (next) {
-            qk(i, k_slot);
-            if (i == tiles - 1) umma_commit(&sm.k_empty[k_slot]);
-          }
-          if (t < 0) continue;
+      // logits two steps ahead of the weights: a buffer of S is free again as
+      // soon as the product of its weights has been issued
+      auto logits = [&](int i, int at, bool first) {  // step k_index + at of tile i
+        const int k = k_index + at, slot = k % kChunkSlots;
+        if (first) {
+          ok = chunk_wait(sm, &sm.k_full[slot], (uint32_t)(k / kChunkSlots) & 1u);
+          if (!ok) return;
+          tc_fence_after();
+        }
+        qk(i, slot);
+        if (i == tiles - 1) umma_commit(&sm.k_empty[slot]);
+      };
+      for (int at = 0; at < min(n, 2) && ok; ++at)
+        for (int i = 0; i < tiles && ok; ++i) logits(i, at, i == 0);
+      for (int t = 0; t < n && ok; ++t, ++k_index) {
+        const int slot = k_index % kChunkSlots;
+        ok = chunk_wait(sm, &sm.v_full[slot], (uint32_t)(k_index / kChunkSlots) & 1u);
+        for (int i = 0; i < tiles && ok; ++i) {
           const uint32_t buf = n_p[i] & 1u, phase = (n_p[i] >> 1) & 1u;
           ++n_p[i];
           if (!(ok = chunk_wait(sm, &sm.p_full[i][buf], phase))) break;
           tc_fence_after();
           pv(i, slot, buf, t > 0);
           if (i == tiles - 1) umma_commit(&sm.v_empty[slot]);
+          if (t + 2 < n) logits(i, 2, i == 0);
         }
-        if (t >= 0) ++k_index;
       }
     } while (ok && walk.next());
     // every product done before the tensor memory is freed

@@ -166,9 +166,10 @@ def attn_bounds(out, lse, info):
     1 +- (2 delta + 2^-20) and rounded once to fp16 (half a step, 2^-11); sums
     of N terms in fp32 add N 2^-24.  The weights -- or weight times page scale,
     in the kernel for many rows -- are held so that a row's largest is at least
-    2^10: below 2^-24 of it one is an fp16 subnormal, whose half step is 2^-25 / 2^10 = 2^-35 of the largest.  The sum
-    of weights is at least the largest weight and a code at most 127, so the N
-    weights of a row add at most N 2^-35 M.
+    2^10: below 2^-24 of it one is an fp16 subnormal, whose half step is
+    2^-25 / 2^10 = 2^-35 of the largest.  The sum of weights is at least the
+    largest weight and a code at most 127, so the N weights of a row add at
+    most N 2^-35 M.
     out is rounded once to bf16 (2^-8 of its value); lse once to fp32."""
     A, S, N, M = info
     D = out.shape[-1]
