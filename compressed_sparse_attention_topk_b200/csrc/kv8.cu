@@ -152,7 +152,7 @@ csa2_status launch_select(const kv8::SelectParams &p, cudaStream_t st) {
 // The kernel of an attention call and its workspace.
 struct AttnPlan {
   bool chunk;      // 256-row tiles on tcgen05
-  int R8;          // else: groups of 8 query rows in a tile
+  int rows;        // else: query rows in a tile
   int ctas;
   size_t part_at;  // the partials, behind one record per CTA
   size_t bytes;
@@ -165,10 +165,10 @@ AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
   AttnPlan a{};
   const int64_t rows = n_sel > 0 ? G : ceil_div(n * G, std::max(B, 1));
   a.chunk = n_sel == 0 && rows > 32;
-  a.R8 = (int)std::max<int64_t>(1, std::min<int64_t>(4, ceil_div(rows, 8)));
-  a.ctas = (a.chunk ? 1 : a.R8 == 1 ? 3 : 2) * device_sms();
+  a.rows = rows <= 4 ? 4 : 8 * (int)std::min<int64_t>(4, ceil_div(rows, 8));
+  a.ctas = (a.chunk ? 1 : a.rows <= 8 ? 3 : 2) * device_sms();
   a.part_at = align_up(size_t(a.ctas) * sizeof(int4), 256);
-  const size_t tile_rows = a.chunk ? kv8::kChunkRows : 8 * a.R8;
+  const size_t tile_rows = a.chunk ? kv8::kChunkRows : a.rows;
   a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * tile_rows * (D + 2) * 4, 256);
   return a;
 }
@@ -201,14 +201,14 @@ csa2_status launch_chunk(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
   return launch_merge<D, kv8::kChunkRows>(p, a, st);
 }
 
-template <int D, int R8, bool P16>
+template <int D, int ROWS, bool P16>
 csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
-  using S = kv8::SplitShape<D, R8>;
+  using S = kv8::SplitShape<D, ROWS>;
   static std::atomic<bool> done[256];  // per device: attributes set
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 256 || !done[dev].load(std::memory_order_acquire)) {
-    if (set_smem_attr(kv8::kv8_split_kernel<D, R8, P16>, S::SMEM, false) != CSA2_OK)
+    if (set_smem_attr(kv8::kv8_split_kernel<D, ROWS, P16>, S::SMEM, false) != CSA2_OK)
       return CSA2_ERR_CUDA;
     if (dev >= 0 && dev < 256) done[dev].store(true, std::memory_order_release);
   }
@@ -220,21 +220,22 @@ csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
     return CSA2_ERR_CUDA;
   {
     TraceScope ts("kv8_attn_split", st);
-    kv8::kv8_split_kernel<D, R8, P16>
+    kv8::kv8_split_kernel<D, ROWS, P16>
         <<<(unsigned)a.ctas, kv8::kSplitThreads, S::SMEM, st>>>(km, vm, p);
     const csa2_status rc = after_launch();
     if (rc != CSA2_OK) return rc;
   }
-  return launch_merge<D, S::ROWS>(p, a, st);
+  return launch_merge<D, ROWS>(p, a, st);
 }
 
 template <int D, bool P16>
 csa2_status launch_attn_d(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
-  switch (a.R8) {
-    case 1: return launch_split<D, 1, P16>(p, a, st);
-    case 2: return launch_split<D, 2, P16>(p, a, st);
-    case 3: return launch_split<D, 3, P16>(p, a, st);
-    default: return launch_split<D, 4, P16>(p, a, st);
+  switch (a.rows) {
+    case 4: return launch_split<D, 4, P16>(p, a, st);
+    case 8: return launch_split<D, 8, P16>(p, a, st);
+    case 16: return launch_split<D, 16, P16>(p, a, st);
+    case 24: return launch_split<D, 24, P16>(p, a, st);
+    default: return launch_split<D, 32, P16>(p, a, st);
   }
 }
 

@@ -115,7 +115,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // Few query rows per sequence (decode, drafts) or a list of blocks per token:
 // the work is the stream of the cache's bytes.
 //
-// A tile is 8 R8 query rows (token-major, the group's heads inside) of one
+// A tile is 4, 8, 16, 24 or 32 query rows (token-major, the group's heads inside) of one
 // sequence and kv head; its keys are cut into units of 32 positions.  The
 // units of all tiles form one line, cut evenly over the CTAs (lengths differ
 // by orders of magnitude between sequences), so a CTA works on the end of a
@@ -129,6 +129,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // heads do not pay for 16, and P^T is an 8 x 8 transpose of S^T).  The tensor
 // work is a fraction of the time the bytes take; a 128-row tcgen05 tile would
 // be mostly padding.
+//
+// What bounds it is the instructions around the products (some 700 of a warp
+// per unit of 8 KB at D = 128, half of them the codes' conversion).  A tile of
+// at most 4 rows therefore takes its logits in whole numbers: a query row is
+// scaled to 23 bits and split into three signed bytes, the columns of a
+// product hold the high and the middle bytes of row t side by side, a second
+// product the low ones, and 2^16 hi + 2^8 mid + lo is the exact dot of the
+// codes themselves, without their conversion (q is off by at most 2^-24 of
+// its row's largest magnitude).  A thread then has one row, so the softmax and
+// the outputs' arithmetic halve too.
 // ---------------------------------------------------------------------------
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = 32 * kSplitWarps;
@@ -136,11 +146,10 @@ constexpr int kUnit = 32;
 constexpr int kNoPos = 1 << 30;  // a table reaches fewer positions; no row sees this one
 constexpr float kPBias = 10.f, kSlack = 5.f;  // weights are at most 2^(10 + 5) < 65504
 
-template <int D, int R8>
+template <int D, int ROWS>
 struct SplitShape {
-  static constexpr int ROWS = 8 * R8;
-  static constexpr int CTAS = R8 == 1 ? 3 : 2;            // per SM
-  static constexpr int STAGES = (R8 == 1 ? 2 : 3) * (128 / D);
+  static constexpr int CTAS = ROWS <= 8 ? 3 : 2;          // per SM
+  static constexpr int STAGES = (ROWS <= 8 ? 2 : 3) * (128 / D);
   static constexpr int TILE = kUnit * D;                  // bytes of a unit's keys (or values)
   static constexpr int RING = STAGES * 2 * TILE;          // per warp
   static constexpr int LDO = D + 4;                       // floats per row of a warp's result
@@ -173,16 +182,19 @@ __device__ __forceinline__ void seq_work(const AttnParams &p, int b, int &tiles,
   units = max(1, (int)((seen + kUnit - 1) / kUnit));
 }
 
-template <int D, int R8, bool P16>
-__global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
+template <int D, int ROWS, bool P16>
+__global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
     kv8_split_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
-  using S = SplitShape<D, R8>;
+  using S = SplitShape<D, ROWS>;
+  constexpr bool QUAD = ROWS == 4;
+  constexpr int R8 = QUAD ? 1 : ROWS / 8;  // groups of 8 columns
+  constexpr int EC = QUAD ? 1 : 2;         // rows of a group that a thread has
   constexpr int DT = D / 16;   // k-steps of a dot; 16-dim tiles of the output
   constexpr int kStages = S::STAGES;
   extern __shared__ unsigned char split_smem[];
   __shared__ uint64_t s_bar[kSplitWarps][kStages];
-  __shared__ float s_z[kSplitWarps][S::ROWS], s_l[kSplitWarps][S::ROWS];
+  __shared__ float s_z[kSplitWarps][ROWS], s_l[kSplitWarps][ROWS];
   __shared__ long long s_sum[kSplitWarps];
   __shared__ long long s_pre;
   __shared__ int s_b;
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
   long long W, u0, u1;
   int b = 0;            // first tile's sequence (dense)
   long long pre = 0;    // units before sequence b
-  const int xt = (p.G + S::ROWS - 1) / S::ROWS;  // tiles of a (token, kv head) with a list
+  const int xt = (p.G + ROWS - 1) / ROWS;  // tiles of a (token, kv head) with a list
   const int list_units = P16 ? (p.n_sel + 1) / 2 : p.n_sel << (p.c.bs_shift - 5);
   if (p.sel) {
     const int64_t tokens = min64(p.s.n, p.s.cu[p.s.B]);
@@ -212,7 +224,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
     long long mine = 0;
     for (int i = tid; i < p.s.B; i += kSplitThreads) {
       int tiles, units, t0, T, pos0;
-      seq_work<S::ROWS>(p, i, tiles, units, t0, T, pos0);
+      seq_work<ROWS>(p, i, tiles, units, t0, T, pos0);
       mine += (long long)tiles * units;
       if (tiles > 0 && blockIdx.x == 0 &&
           (int64_t)p.s.lens[i] > ((int64_t)p.s.width << p.c.bs_shift))
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       long long w = 0;
       if (i < p.s.B) {
         int tiles, units, t0, T, pos0;
-        seq_work<S::ROWS>(p, i, tiles, units, t0, T, pos0);
+        seq_work<ROWS>(p, i, tiles, units, t0, T, pos0);
         w = (long long)tiles * units * p.c.Hk;
       }
       const long long incl = warp_incl_scan64(w);
@@ -296,25 +308,25 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       tl.tok0 = (int)tok;
       tl.pos0 = (int)max((int64_t)-0x40000000,
                          (int64_t)p.s.lens[tl.b] - p.s.cu[tl.b + 1] + tok);
-      tl.row0 = x * S::ROWS;
-      tl.nrows = min(S::ROWS, p.G - tl.row0);
+      tl.row0 = x * ROWS;
+      tl.nrows = min(ROWS, p.G - tl.row0);
       tl.units = list_units;
       list_at = (tok * p.c.Hk + tl.h) * p.n_sel;
     } else {
       int tiles, units, t0, T, pos0;
-      seq_work<S::ROWS>(p, b, tiles, units, t0, T, pos0);
+      seq_work<ROWS>(p, b, tiles, units, t0, T, pos0);
       while (u - pre >= (long long)tiles * units * p.c.Hk) {
         pre += (long long)tiles * units * p.c.Hk;
         ++b;
-        seq_work<S::ROWS>(p, b, tiles, units, t0, T, pos0);
+        seq_work<ROWS>(p, b, tiles, units, t0, T, pos0);
       }
       const long long idx = (u - pre) / units;
       tile_begin = pre + idx * units;
       const int x = (int)(idx / p.c.Hk);
       tl.b = b;
       tl.h = (int)(idx - (long long)x * p.c.Hk);
-      tl.row0 = x * S::ROWS;
-      tl.nrows = min(S::ROWS, T * p.G - tl.row0);
+      tl.row0 = x * ROWS;
+      tl.nrows = min(ROWS, T * p.G - tl.row0);
       tl.tok0 = t0;
       tl.pos0 = pos0;
       tl.units = units;
@@ -324,19 +336,21 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
     const int first = (int)(u - tile_begin);
     const int last = (int)min(u1 - tile_begin, (long long)tl.units);  // units [first, last)
 
-    // ---- query rows: power-of-two scaled fp16 fragments.  Thread (g, t)
-    // holds row g of each group of 8, dims 64 hh + 16 t + 4 w + (0, 2 | 1, 3)
-    // for k-step 4 hh + w, as the cache's words below ----
+    // ---- query rows.  Thread (g, t) holds dims 64 hh + 16 t + 4 w + 0 .. 3
+    // for k-step 4 hh + w, as the cache's words below: of row g of each group
+    // of 8, power-of-two scaled fp16 (0, 2 | 1, 3); or (QUAD) of row g / 2,
+    // bytes: high (g even) or middle (g odd), and low (g even) ----
     uint32_t qb[R8][DT][2];
-    float fac[R8][2];     // of rows 2 t, 2 t + 1: the columns of S^T and O^T
-    int row_pos[R8][2];
+    float fac[R8][EC];     // of the thread's rows: the columns of S^T and O^T
+    int row_pos[R8][EC];
 #pragma unroll
     for (int q8 = 0; q8 < R8; ++q8) {
-      const int R = tl.row0 + min(q8 * 8 + g, tl.nrows - 1);
+      const int R = tl.row0 + min(QUAD ? g >> 1 : q8 * 8 + g, tl.nrows - 1);
       const int tok = R / p.G;
       const uint16_t *src = p.q + (int64_t)(tl.tok0 + tok) * p.q_stride +
                             (int64_t)(tl.h * p.G + R - tok * p.G) * D;
       float big = 0.f;
+      bool finite = true;
 #pragma unroll
       for (int hh = 0; hh < D / 64; ++hh) {
         const uint4 a = *reinterpret_cast<const uint4 *>(src + 64 * hh + 16 * t);
@@ -344,9 +358,11 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
         const uint32_t ws[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+          const float x0 = fabsf(__uint_as_float(ws[e] << 16));
+          const float x1 = fabsf(__uint_as_float(ws[e] & 0xffff0000u));
           qb[q8][hh * 4 + e / 2][e & 1] = ws[e];
-          big = fmaxf(big, fabsf(__uint_as_float(ws[e] << 16)));
-          big = fmaxf(big, fabsf(__uint_as_float(ws[e] & 0xffff0000u)));
+          big = fmaxf(big, fmaxf(x0, x1));
+          finite &= x0 < INFINITY && x1 < INFINITY;
         }
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
@@ -356,34 +372,59 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       const uint32_t sb =
           min((big > 0.f && eb < 255u) ? max(254u - eb, 1u) : 127u, 253u);
       const float down = __uint_as_float(sb << 23);
-      const float f = p.sm_scale * 1.44269504088896340736f * __uint_as_float((254u - sb) << 23);
+      float f = p.sm_scale * 1.44269504088896340736f * __uint_as_float((254u - sb) << 23);
+      if constexpr (QUAD) {
+        f *= 0x1p-21f;  // the digits stand for 2^22 times half the scaled value
+        // bytes carry no NaN or infinity: the row's scale does
+        const uint32_t who = __ballot_sync(0xffffffffu, finite);
+        if ((who >> (lane & 28) & 15u) != 15u) f = __int_as_float(0x7fffffff);
+      }
       const int pos = min(tl.pos0 + tok, kNoPos - 1);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < EC; ++e) {
         fac[q8][e] = __shfl_sync(0xffffffffu, f, (2 * t + e) * 4);
         row_pos[q8][e] = __shfl_sync(0xffffffffu, pos, (2 * t + e) * 4);
       }
 #pragma unroll
       for (int s = 0; s < DT; ++s) {
         const uint32_t w0 = qb[q8][s][0], w1 = qb[q8][s][1];  // dims 0, 1 and 2, 3
-        qb[q8][s][0] = pack_f16(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down);
-        qb[q8][s][1] = pack_f16(__uint_as_float(w0 & 0xffff0000u) * down,
-                                __uint_as_float(w1 & 0xffff0000u) * down);
+        if constexpr (QUAD) {
+          const float y[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
+                              __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)};
+          uint32_t upper = 0u, low = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int whole = __float2int_rn(y[e] * down * 0x1p21f);  // |.| <= 2^22
+            const int d0 = (int8_t)whole, rest = (whole - d0) >> 8;
+            const int d1 = (int8_t)rest, d2 = (rest - d1) >> 8;      // |d2| <= 64
+            upper |= (uint32_t)(uint8_t)(g & 1 ? d1 : d2) << (8 * e);
+            low |= (uint32_t)(uint8_t)(g & 1 ? 0 : d0) << (8 * e);
+          }
+          qb[q8][s][0] = upper;
+          qb[q8][s][1] = low;
+        } else {
+          qb[q8][s][0] =
+              pack_f16(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down);
+          qb[q8][s][1] = pack_f16(__uint_as_float(w0 & 0xffff0000u) * down,
+                                  __uint_as_float(w1 & 0xffff0000u) * down);
+        }
       }
     }
 
     // ---- state: weights are 2^(x - z); one above 2^lim moves z (any does
     // where z is not set yet) ----
-    float o[R8][DT][4], lim[R8][2], z[R8][2], l[R8][2];
+    float o[R8][DT][2 * EC], lim[R8][EC], z[R8][EC], l[R8][EC];
 #pragma unroll
     for (int q8 = 0; q8 < R8; ++q8) {
 #pragma unroll
       for (int j = 0; j < DT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[q8][j][e] = 0.f;
-      lim[q8][0] = lim[q8][1] = -INFINITY;
-      z[q8][0] = z[q8][1] = 0.f;
-      l[q8][0] = l[q8][1] = 0.f;
+        for (int e = 0; e < 2 * EC; ++e) o[q8][j][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < EC; ++e) {
+        lim[q8][e] = -INFINITY;
+        z[q8][e] = l[q8][e] = 0.f;
+      }
     }
 
     // ---- this warp's units: first + warp, + kSplitWarps, ... ----
@@ -489,64 +530,83 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       if (any) {
         const unsigned char *kt = ring + st * 2 * S::TILE, *vt = kt + S::TILE;
         // ---- S^T = K Q^T: 16 positions per row tile ----
-        float sc[R8][2][4];
+        float sc[R8][2][2 * EC];  // [..][16 positions][position g, g + 8][row]
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = k * 16 + g;  // and r + 8: the same place in the swizzle
+          float dot[R8][4];
+          int32_t upper[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int hh = 0; hh < D / 64; ++hh) {
             const int chunk = D == 128 ? ((t + 4 * hh) ^ g) : (t ^ ((g >> 1) & 3));
             const uint4 x = *reinterpret_cast<const uint4 *>(kt + r * D + chunk * 16);
             const uint4 y = *reinterpret_cast<const uint4 *>(kt + (r + 8) * D + chunk * 16);
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            if constexpr (QUAD) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t a[4] = {codes_f16(xs[w], flip), codes_f16(ys[w], flip),
-                                     codes_f16(xs[w] >> 8, flip), codes_f16(ys[w] >> 8, flip)};
+              for (int w = 0; w < 4; w += 2) {
+                const uint32_t a[4] = {xs[w], ys[w], xs[w + 1], ys[w + 1]};
+                mma_i8<false>(upper, a, qb[0][hh * 4 + w][0], qb[0][hh * 4 + w + 1][0]);
+                mma_i8<false>(low, a, qb[0][hh * 4 + w][1], qb[0][hh * 4 + w + 1][1]);
+              }
+            } else {
 #pragma unroll
-              for (int q8 = 0; q8 < R8; ++q8) {
-                if (hh == 0 && w == 0)
-                  mma_f16_first(sc[q8][k], a, qb[q8][0][0], qb[q8][0][1]);
-                else
-                  mma_f16(sc[q8][k], a, qb[q8][hh * 4 + w][0], qb[q8][hh * 4 + w][1]);
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t a[4] = {codes_f16(xs[w], flip), codes_f16(ys[w], flip),
+                                       codes_f16(xs[w] >> 8, flip), codes_f16(ys[w] >> 8, flip)};
+#pragma unroll
+                for (int q8 = 0; q8 < R8; ++q8) {
+                  if (hh == 0 && w == 0)
+                    mma_f16_first(dot[q8], a, qb[q8][0][0], qb[q8][0][1]);
+                  else
+                    mma_f16(dot[q8], a, qb[q8][hh * 4 + w][0], qb[q8][hh * 4 + w][1]);
+                }
               }
             }
           }
+          // x - z, a thread's positions g, g + 8 and rows (2 t, 2 t + 1 of each
+          // group, or t)
+#pragma unroll
+          for (int q8 = 0; q8 < R8; ++q8)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int e = 0; e < EC; ++e) {
+                float x;
+                if constexpr (QUAD)  // 2^16 hi + 2^8 mid < 2^29
+                  x = fmaf((float)(upper[2 * half] * 256 + upper[2 * half + 1]), 256.f,
+                           (float)low[2 * half]);
+                else
+                  x = dot[q8][half * 2 + e];
+                sc[q8][k][half * EC + e] = fmaf(x, fac[q8][e] * ks[k], -z[q8][e]);
+              }
         }
-        // ---- softmax: a thread has positions g, g + 8 of each 16 and rows
-        // 2 t, 2 t + 1 of each 8 ----
-#pragma unroll
-        for (int q8 = 0; q8 < R8; ++q8)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[q8][k][e] = fmaf(sc[q8][k][e], fac[q8][e & 1] * ks[k], -z[q8][e & 1]);
+        // ---- softmax ----
         if (max(pos[0], pos[1]) + 15 > tl.pos_first) {  // not seen whole by every row
 #pragma unroll
           for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (pos[k] + g + (e >> 1) * 8 > row_pos[q8][e & 1]) sc[q8][k][e] = -INFINITY;
+              for (int e = 0; e < 2 * EC; ++e)
+                if (pos[k] + g + (e / EC) * 8 > row_pos[q8][e % EC]) sc[q8][k][e] = -INFINITY;
         }
-        float top[R8][2];
+        float top[R8][EC];
         bool move = false;
 #pragma unroll
         for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            top[q8][e] = fmaxf(fmaxf(sc[q8][0][e], sc[q8][0][e + 2]),
-                               fmaxf(sc[q8][1][e], sc[q8][1][e + 2]));
+          for (int e = 0; e < EC; ++e) {
+            top[q8][e] = fmaxf(fmaxf(sc[q8][0][e], sc[q8][0][EC + e]),
+                               fmaxf(sc[q8][1][e], sc[q8][1][EC + e]));
             move |= top[q8][e] > lim[q8][e];
           }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
           for (int q8 = 0; q8 < R8; ++q8) {
-            float corr[2];
+            float corr[EC];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < EC; ++e) {
               float mx = top[q8][e];
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -561,29 +621,32 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                   sc[q8][k][e] -= by;
-                  sc[q8][k][e + 2] -= by;
+                  sc[q8][k][EC + e] -= by;
                 }
               }
             }
 #pragma unroll
             for (int j = 0; j < DT; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[q8][j][e] *= corr[e & 1];
+              for (int e = 0; e < 2 * EC; ++e) o[q8][j][e] *= corr[e % EC];
           }
         }
+        // weights; QUAD: row t in column 2 t, zeros beside it
         uint32_t pb[R8][2][2];
 #pragma unroll
         for (int q8 = 0; q8 < R8; ++q8) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[q8][k][e] = ex2(sc[q8][k][e]);
-            pb[q8][k][0] = transpose_8x8(pack_f16(sc[q8][k][0], sc[q8][k][1]));
-            pb[q8][k][1] = transpose_8x8(pack_f16(sc[q8][k][2], sc[q8][k][3]));
+            for (int e = 0; e < 2 * EC; ++e) sc[q8][k][e] = ex2(sc[q8][k][e]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              pb[q8][k][half] = transpose_8x8(
+                  pack_f16(sc[q8][k][half * EC], QUAD ? 0.f : sc[q8][k][half * EC + EC - 1]));
           }
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            l[q8][e] += (sc[q8][0][e] + sc[q8][0][e + 2]) + (sc[q8][1][e] + sc[q8][1][e + 2]);
+          for (int e = 0; e < EC; ++e)
+            l[q8][e] += (sc[q8][0][e] + sc[q8][0][EC + e]) + (sc[q8][1][e] + sc[q8][1][EC + e]);
         }
         // ---- O^T += vs * V^T P^T: rows g and g + 8 of 16-dim tile j are
         // dims g DT 2 + j and + DT + j, so a thread's bytes of a token are
@@ -631,8 +694,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 #pragma unroll
               for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  o[q8][j][e] = fmaf(vs[k], part[q8][e], o[q8][j][e]);
+                for (int e = 0; e < 2 * EC; ++e)
+                  o[q8][j][e] = fmaf(vs[k], part[q8][(e / EC) * 2 + e % EC], o[q8][j][e]);
             }
           }
         }
@@ -647,12 +710,12 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 #pragma unroll
     for (int q8 = 0; q8 < R8; ++q8)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < EC; ++e) {
         float sum = l[q8][e];
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int r = q8 * 8 + 2 * t + e;
+        const int r = QUAD ? t : q8 * 8 + 2 * t + e;
         if (g == 0) {
           s_z[warp][r] = sum == 0.f ? -INFINITY : z[q8][e];
           s_l[warp][r] = sum;
@@ -662,8 +725,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
 #pragma unroll
           for (int j = 0; j < DT; j += 4)
             *reinterpret_cast<float4 *>(res + r * S::LDO + (2 * g + half) * DT + j) = make_float4(
-                o[q8][j][half * 2 + e], o[q8][j + 1][half * 2 + e], o[q8][j + 2][half * 2 + e],
-                o[q8][j + 3][half * 2 + e]);
+                o[q8][j][half * EC + e], o[q8][j + 1][half * EC + e],
+                o[q8][j + 2][half * EC + e], o[q8][j + 3][half * EC + e]);
       }
     __syncthreads();
     const bool whole = first == 0 && last == tl.units;
@@ -703,8 +766,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, R8>::CTAS)
       } else {
         *reinterpret_cast<float4 *>(part + r * D + d) = acc;
         if (d == 0) {
-          part[S::ROWS * D + r] = mx;
-          part[S::ROWS * D + S::ROWS + r] = sum;
+          part[ROWS * D + r] = mx;
+          part[ROWS * D + ROWS + r] = sum;
         }
       }
     }
