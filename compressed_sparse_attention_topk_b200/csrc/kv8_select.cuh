@@ -45,6 +45,7 @@ __device__ __forceinline__ int seen_blocks(int64_t pos, int shift, int width) {
 template <int D, int R>
 __global__ void __launch_bounds__(kScoreThreads, 2) kv8_score_kernel(const SelectParams p) {
   constexpr int TT = 8 * R;
+  static_assert(TT == kScoreWarps * R, "R tokens per warp");
   constexpr int KS = D / 32;       // k-steps
   constexpr int LD = D + 32;       // bytes per token of q8: its reads meet no bank twice
   __shared__ __align__(16) int8_t s_q[TT][LD];
@@ -108,45 +109,60 @@ __global__ void __launch_bounds__(kScoreThreads, 2) kv8_score_kernel(const Selec
     load();
   }
 
-  // ---- the tokens' group queries in 8 bits ----
-  for (int i = warp; i < TT; i += kScoreWarps) {
-    float qs[D / 32];
+  // ---- the tokens' group queries in 8 bits: R tokens per warp, their heads'
+  // loads in flight together, four heads at a time ----
+  constexpr int E = D / 32;  // dims per lane
+  double sum[R][E];
+#pragma unroll
+  for (int x = 0; x < R; ++x)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[x][e] = 0.0;
+  for (int k0 = 0; k0 < p.G; k0 += 4) {
+    uint32_t w[R][4][E / 2];
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const int i = warp + x * kScoreWarps;
+      const uint16_t *src =
+          p.q + (tok0 + i) * p.q_stride + ((int64_t)h * p.G + k0) * D + lane * E;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = i < count && k0 + k < p.G;
+        if constexpr (D == 128) {
+          const uint2 y = in ? *reinterpret_cast<const uint2 *>(src + k * D) : make_uint2(0u, 0u);
+          w[x][k][0] = y.x;
+          w[x][k][E / 2 - 1] = y.y;
+        } else {
+          w[x][k][0] = in ? *reinterpret_cast<const uint32_t *>(src + k * D) : 0u;
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < R; ++x)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          sum[x][2 * e] += (double)__uint_as_float(w[x][k][e] << 16);
+          sum[x][2 * e + 1] += (double)__uint_as_float(w[x][k][e] & 0xffff0000u);
+        }
+  }
+#pragma unroll
+  for (int x = 0; x < R; ++x) {
+    const int i = warp + x * kScoreWarps;
+    float qs[E];
     float big = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) qs[e] = 0.f;
-    if (i < count) {
-      double sum[D / 32];
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) sum[e] = 0.0;
-      const uint16_t *src = p.q + (tok0 + i) * p.q_stride + (int64_t)h * p.G * D + lane * (D / 32);
-      for (int k = 0; k < p.G; ++k) {
-        uint32_t w[D / 64];
-        if constexpr (D == 128) {
-          const uint2 y = *reinterpret_cast<const uint2 *>(src + (int64_t)k * D);
-          w[0] = y.x;
-          w[D / 64 - 1] = y.y;
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t *>(src + (int64_t)k * D);
-        }
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-          sum[2 * e] += (double)__uint_as_float(w[e] << 16);
-          sum[2 * e + 1] += (double)__uint_as_float(w[e] & 0xffff0000u);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        qs[e] = (float)sum[e];
-        const float a = fabsf(qs[e]);
-        big = fmaxf(big, a == a ? a : INFINITY);
-      }
+    for (int e = 0; e < E; ++e) {
+      qs[e] = (float)sum[x][e];
+      const float a = fabsf(qs[e]);
+      big = fmaxf(big, a == a ? a : INFINITY);
     }
     big = warp_max(big);
     const bool dead = !(big > 0.f && big < INFINITY);
     const float r = dead ? 0.f : __fdiv_rn(127.f, big);
     uint32_t word = 0u;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int q8 = dead ? 0 : __float2int_rn(__fmul_rn(qs[e], r));
       word |= (uint32_t)(uint8_t)(int8_t)q8 << (8 * e);
     }
@@ -164,7 +180,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) kv8_score_kernel(const Selec
       qb[r][s][1] = y.y;
     }
 
-  // ---- 16 blocks at a time ----
+  // ---- 16 blocks at a time; this thread's tokens are 2 t, 2 t + 1 of each 8 ----
+  const int row_step = p.c.Hk * p.s.width;  // < 2^23 floats from token to token
+  const int mine = count - 2 * t;           // r * 8 + e < mine: it is one of the tile's
+  float *const rows = p.scores + ((tok0 + 2 * t) * p.c.Hk + h) * p.s.width;
   for (; gi < groups; gi += stride) {
     int32_t acc[R][4];  // 256 times the high bytes' dots, then the low bytes' on top
 #pragma unroll
@@ -201,18 +220,20 @@ __global__ void __launch_bounds__(kScoreThreads, 2) kv8_score_kernel(const Selec
       pages(gi + stride);
       load();
     }
+    float *at = rows + j0;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int half = 0; half < 2; ++half, at += 8) {
+      if (j0 + 8 * half >= nblk) break;
+      const float kk = half ? k1 : k0;
+      const bool bad = half ? bad1 : bad0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = r * 8 + 2 * t + (e & 1), j = j0 + (e >> 1) * 8;
-        if (i < count && j < nblk) {
-          const float dot = (float)acc[r][e];
-          const float sc = __fadd_rn(__fmul_rn(dot, (e >> 1) ? k1 : k0), 0.f);
-          p.scores[((tok0 + i) * p.c.Hk + h) * p.s.width + j] =
-              ((e >> 1) ? bad1 : bad0) ? -INFINITY : sc;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float sc = __fadd_rn(__fmul_rn((float)acc[r][half * 2 + e], kk), 0.f);
+          if (r * 8 + e < mine) at[(r * 8 + e) * row_step] = bad ? -INFINITY : sc;
         }
-      }
+    }
   }
 }
 
