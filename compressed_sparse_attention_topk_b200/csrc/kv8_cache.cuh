@@ -179,8 +179,29 @@ struct AppendParams {
   int32_t group;  // tokens per CTA
 };
 
-__device__ __forceinline__ int kv8_code(float x, float s) {
-  return max(-127, min(127, __float2int_rn(__fdiv_rn(x, s))));
+// rint(x / s) of eight values (two to a word), |x| <= 127 s.  inv = fl(1 / s), or
+// NaN for s below 2^-100.  x inv is within 127 2^-24 of x / s, and the rounded
+// quotient within 127 2^-25: unless x inv lies within 2^-14 of a half, both
+// round to the integer n that adding 1.5 2^23 leaves in the low bits; where one
+// of the eight does, or is not finite, the divisions decide.
+__device__ __forceinline__ void kv8_codes(const uint32_t (&w)[4], float s, float inv,
+                                          int32_t (&c)[8]) {
+  constexpr float kMagic = 12582912.f;
+  bool sure = true;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    const float t = fmaf(x, inv, kMagic);
+    const float n = t - kMagic;
+    sure &= fabsf(fmaf(x, inv, -n)) <= 0.5f - 0x1p-14f;
+    c[e] = __float_as_int(t) - __float_as_int(kMagic);
+  }
+  if (sure) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    c[e] = max(-127, min(127, __float2int_rn(__fdiv_rn(x, s))));
+  }
 }
 
 template <int D, int BS>
@@ -275,6 +296,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
     const float s = fmaxf(s_old, __fdiv_rn(big, 127.f));
     const bool grew = s > s_old;
     const float ratio = grew ? __fdiv_rn(s_old, s) : 1.f;
+    const float inv = s >= 0x1p-100f ? __fdiv_rn(1.f, s) : __int_as_float(0x7fffffff);
     if (tid == 0) {
       *scale_at = s;
       s_len[(turn & 1) ^ 1] = BS;
@@ -286,19 +308,21 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
       if (r >= end) continue;
       const bool old = r < r0;
       const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+      int32_t cs[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (old) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          cs[e] = (int8_t)(w[e >> 2] >> (8 * (e & 3)));
+          if (grew) cs[e] = __float2int_rn(__fmul_rn((float)cs[e], ratio));
+        }
+      } else if (s > 0.f) {
+        kv8_codes(w, s, inv, cs);
+      }
       uint32_t o[2] = {0u, 0u};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        int c;
-        if (old) {
-          c = (int8_t)(w[e >> 2] >> (8 * (e & 3)));
-          if (grew) c = __float2int_rn(__fmul_rn((float)c, ratio));
-        } else {
-          const uint32_t bits = (e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16);
-          c = s > 0.f ? kv8_code(__uint_as_float(bits), s) : 0;
-        }
-        o[e >> 2] |= (uint32_t)(uint8_t)c << (8 * (e & 3));
-        sum[e] += c;
+        o[e >> 2] |= (uint32_t)(uint8_t)cs[e] << (8 * (e & 3));
+        sum[e] += cs[e];
       }
       if (!old || grew)
         *reinterpret_cast<uint2 *>(codes + r * D + col) = make_uint2(o[0], o[1]);
