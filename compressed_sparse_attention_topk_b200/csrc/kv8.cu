@@ -176,11 +176,12 @@ AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
 
 // Merges the tiles that several CTAs shared; its blocks come up while the
 // attention kernel's last ones run.
-template <int D, int ROWS>
+template <int D, int ROWS, int RPB>
 csa2_status launch_merge(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
   TraceScope ts("kv8_attn_merge", st);
-  return launch_dependent(kv8::kv8_merge_kernel<D, ROWS>, dim3((unsigned)a.ctas, ROWS / kv8::merge_rows(ROWS)),
-                          kv8::kMergeThreads, 0, st, p, a.ctas);
+  return launch_dependent(kv8::kv8_merge_kernel<D, ROWS, RPB>,
+                          dim3((unsigned)a.ctas, ROWS / RPB), kv8::kMergeThreads, 0, st, p,
+                          a.ctas);
 }
 
 template <int D>
@@ -199,7 +200,7 @@ csa2_status launch_chunk(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
     const csa2_status rc = after_launch();
     if (rc != CSA2_OK) return rc;
   }
-  return launch_merge<D, kv8::kChunkRows>(p, a, st);
+  return launch_merge<D, kv8::kChunkRows, 32>(p, a, st);
 }
 
 template <int D, int ROWS, bool P16>
@@ -226,7 +227,12 @@ csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
     const csa2_status rc = after_launch();
     if (rc != CSA2_OK) return rc;
   }
-  return launch_merge<D, ROWS>(p, a, st);
+  // at most this many tiles share the CTAs: with few, a row has hundreds of
+  // partials, and a block to itself (one sequence and kv head of 262,144
+  // positions: 66 us with four rows to a block)
+  const int64_t tiles = (p.s.n * p.G / ROWS + p.s.B) * p.c.Hk;
+  return tiles * 32 <= a.ctas ? launch_merge<D, ROWS, 1>(p, a, st)
+                              : launch_merge<D, ROWS, 4>(p, a, st);
 }
 
 template <int D, bool P16>

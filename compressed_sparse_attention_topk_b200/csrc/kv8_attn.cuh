@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
   extern __shared__ unsigned char split_smem[];
   __shared__ uint64_t s_bar[kSplitWarps][kStages];
   __shared__ float s_z[kSplitWarps][ROWS], s_l[kSplitWarps][ROWS];
-  __shared__ long long s_sum[kSplitWarps];
+  __shared__ long long s_sum[kSplitWarps], s_tiles[kSplitWarps];
   __shared__ long long s_pre;
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -212,45 +212,58 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
   asm volatile("mov.b32 %0, %1;" : "=r"(flip) : "n"(kFlip));
 
   // ---- the line of units: its length, and this CTA's stretch of it ----
-  long long W, u0, u1;
+  long long W, u0, u1, n_tiles = 0;
   int b = 0;            // first tile's sequence (dense)
   long long pre = 0;    // units before sequence b
   const int xt = (p.G + ROWS - 1) / ROWS;  // tiles of a (token, kv head) with a list
   const int list_units = P16 ? (p.n_sel + 1) / 2 : p.n_sel << (p.c.bs_shift - 5);
   if (p.sel) {
     const int64_t tokens = min64(p.s.n, p.s.cu[p.s.B]);
-    W = max((long long)tokens, 0ll) * p.c.Hk * xt * list_units;
+    n_tiles = max((long long)tokens, 0ll) * p.c.Hk * xt;
+    W = n_tiles * list_units;
   } else {
-    long long mine = 0;
+    long long mine = 0, count = 0;
     for (int i = tid; i < p.s.B; i += kSplitThreads) {
       int tiles, units, t0, T, pos0;
       seq_work<ROWS>(p, i, tiles, units, t0, T, pos0);
       mine += (long long)tiles * units;
+      count += tiles;
       if (tiles > 0 && blockIdx.x == 0 &&
           (int64_t)p.s.lens[i] > ((int64_t)p.s.width << p.c.bs_shift))
         raise_status(kStatusBadIndex);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
+    for (int o = 16; o > 0; o >>= 1) {
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    if (lane == 0) {
+      s_sum[warp] = mine;
+      s_tiles[warp] = count;
+    }
     __syncthreads();
     W = 0;
-    for (int w = 0; w < kSplitWarps; ++w) W += s_sum[w];
+    for (int w = 0; w < kSplitWarps; ++w) {
+      W += s_sum[w];
+      n_tiles += s_tiles[w];
+    }
     W *= p.c.Hk;
+    n_tiles *= p.c.Hk;
   }
-  // a CTA gets at least one unit per warp
-  const long long ctas = max(1ll, min((long long)gridDim.x, (W + kSplitWarps - 1) / kSplitWarps));
+  // as many CTAs as there are, but no tile in pieces of fewer units than two
+  // for each warp (every piece is a partial to merge)
+  const long long ctas =
+      max(1ll, min((long long)gridDim.x, max(n_tiles, W / (2 * kSplitWarps))));
   const long long c = blockIdx.x;
   u0 = c < ctas ? W * c / ctas : W;
   u1 = c < ctas ? W * (c + 1) / ctas : W;
-  if (p.sel && W > 0 && W / list_units * 2 <= gridDim.x) {
+  if (p.sel && W > 0 && n_tiles * 2 <= gridDim.x) {
     // few lists, all as long: the same number of CTAs for each, so that none
     // works on two
-    const long long lists = W / list_units;
-    const long long each = min((long long)gridDim.x / lists,
-                               max(1ll, (long long)list_units / kSplitWarps));
+    const long long each = min((long long)gridDim.x / n_tiles,
+                               max(1ll, (long long)list_units / (2 * kSplitWarps)));
     u0 = u1 = W;
-    if (c < lists * each) {
+    if (c < n_tiles * each) {
       u0 = c / each * list_units + list_units * (c % each) / each;
       u1 = c / each * list_units + list_units * (c % each + 1) / each;
     }
@@ -791,18 +804,17 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
 // ---------------------------------------------------------------------------
 // Tiles of ROWS query rows that several CTAs shared (of kv8_split_kernel, or
 // of kv8_chunk_kernel): block (c, y) merges rows RPB y .. of the tile that CTA
-// c begins and later CTAs end, in CTA order.  WPR warps share a row's
-// partials, eight in flight each: two for a few rows with many partials, one
-// for a chunk's 256 rows with few.
+// c begins and later CTAs end, in CTA order.  RPB 32: a warp takes a row at a
+// time (a chunk's 256 rows, of few partials each).  RPB 4 and 1: the block's
+// warps share a row's partials, eight, four or two to a row, as many rows as
+// the block has; RPB 1 where so few tiles share the CTAs that a row can have
+// hundreds of partials.
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
-constexpr int merge_rows(int rows) { return rows > 32 ? 32 : 4; }  // per block
 
-template <int D, int ROWS>
+template <int D, int ROWS, int RPB>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int ctas) {
   constexpr size_t PART = size_t(ROWS) * (D + 2);
-  constexpr int RPB = ROWS > 32 ? 32 : 4;
-  constexpr int WPR = RPB == 4 ? 2 : 1;
   constexpr int E = D / 32;
   __shared__ float s_o[8][D], s_ml[8][2];
   const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -821,11 +833,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
     }
   }
   const int count = min(end, ctas - 1) - c + 1;
-  const int half = (count + WPR - 1) / WPR;
-  const int k0 = (warp % WPR) * half, k1 = min(count, k0 + half);
+  const int here = min(RPB, nrows - (int)blockIdx.y * RPB);
+  const int wpr = RPB > 4 ? 1 : here == 1 ? 8 : here == 2 ? 4 : 2;  // warps per row
+  const int piece = (count + wpr - 1) / wpr;
+  const int k0 = (warp % wpr) * piece, k1 = min(count, k0 + piece);
   auto at = [&](int k) { return p.part + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * PART; };
 #pragma unroll 1
-  for (int r = blockIdx.y * RPB + warp / WPR; r < (int)(blockIdx.y + 1) * RPB; r += 8 / WPR) {
+  for (int r = blockIdx.y * RPB + warp / wpr; r < (int)(blockIdx.y + 1) * RPB; r += 8 / wpr) {
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -843,7 +857,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
       }
     }
     float sum = l, zero = m == -INFINITY ? 0.f : m;
-    if constexpr (WPR == 2) {  // (one row per pair of warps: no second turn)
+    if constexpr (RPB <= 4) {  // (one turn of the loop: 8 / wpr rows are all there are)
 #pragma unroll
       for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
       if (lane == 0) {
@@ -851,26 +865,34 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
         s_ml[warp][1] = l;
       }
       __syncthreads();
-      if (warp & 1) return;
-      const float m1 = s_ml[warp + 1][0], mx = fmaxf(m, m1);
+      if (warp % wpr) return;
+      float mx = m;
+      for (int w = 1; w < wpr; ++w) mx = fmaxf(mx, s_ml[warp + w][0]);
       zero = mx == -INFINITY ? 0.f : mx;
-      const float f0 = ex2(m - zero);
-      const float f1 = ex2(m1 - zero);
-      sum = l * f0 + s_ml[warp + 1][1] * f1;
+      float f = ex2(m - zero);
+      sum = l * f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + s_o[warp + 1][lane * E + e] * f1;
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      for (int w = 1; w < wpr; ++w) {
+        f = ex2(s_ml[warp + w][0] - zero);
+        sum = fmaf(s_ml[warp + w][1], f, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[warp + w][lane * E + e], f, o[e]);
+      }
     }
-    if (r >= nrows) continue;
-    const int R = rec.w + r, tok = R / p.G;
-    const int64_t row =
-        (int64_t)(rec.x + tok) * (p.G * p.c.Hk) + (rec.y & 255) * p.G + R - tok * p.G;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (r < nrows) {
+      const int R = rec.w + r, tok = R / p.G;
+      const int64_t row =
+          (int64_t)(rec.x + tok) * (p.G * p.c.Hk) + (rec.y & 255) * p.G + R - tok * p.G;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      p.out[row * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16(o[e] * inv));
-    if (lane == 0 && p.lse)
-      p.lse[row] =
-          sum == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(sum));
+      for (int e = 0; e < E; ++e)
+        p.out[row * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16(o[e] * inv));
+      if (lane == 0 && p.lse)
+        p.lse[row] =
+            sum == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(sum));
+    }
+    if constexpr (RPB <= 4) return;
   }
 }
 

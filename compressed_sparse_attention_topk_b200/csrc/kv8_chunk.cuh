@@ -67,7 +67,7 @@ struct ChunkSmem {
   uint64_t meta_full[kMetaSlots], drained;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
-  long long sum[kChunkThreads / 32];
+  long long sum[kChunkThreads / 32], tiles[kChunkThreads / 32];
   long long pre;
   int b;
 };
@@ -350,20 +350,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     fence_barrier_init();
   }
   // ---- this CTA's stretch of the line ----
-  long long mine = 0;
+  long long mine = 0, tiles = 0;
   for (int b = tid; b < p.s.B; b += kChunkThreads) {
     const ChunkSeq s = chunk_seq(p, b);
+    tiles += s.tiles;
     for (int x = 0; x < s.tiles; ++x) mine += chunk_steps(s, p.G, x);
     if (s.tiles > 0 && blockIdx.x == 0 && p.s.lens[b] > s.reach) raise_status(kStatusBadIndex);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sm.sum[warp] = mine;
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  if (lane == 0) {
+    sm.sum[warp] = mine;
+    sm.tiles[warp] = tiles;
+  }
   __syncthreads();
   long long W = 0;
-  for (int w = 0; w < kWarps; ++w) W += sm.sum[w];
+  tiles = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    W += sm.sum[w];
+    tiles += sm.tiles[w];
+  }
   W *= p.c.Hk;
-  const long long ctas = max(1ll, min((long long)gridDim.x, (W + 3) / 4));
+  // as many CTAs as there are, but no tile in pieces of fewer than 8 steps
+  const long long ctas = max(1ll, min((long long)gridDim.x, max(tiles * p.c.Hk, W / 8)));
   const long long c = blockIdx.x;
   const long long u0 = c < ctas ? W * c / ctas : W, u1 = c < ctas ? W * (c + 1) / ctas : W;
   if (u0 >= u1) {
@@ -428,6 +440,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const int tok = R / p.G;
       const int64_t head = (int64_t)walk.h * p.G + R - tok * p.G;
       const int my_pos = min(walk.s.pos0 + tok, kNoPos - 1);
+      const float vref = chunk_vref(p, walk.b, walk.h);
       float f;  // logit per product, without the page's key scale
       {
         const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -547,7 +560,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       bool ok = chunk_wait(sm, &sm.o_done[tile][(n_steps - 1) & 1u], ((n_steps - 1) >> 1) & 1u);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const float vref = chunk_vref(p, walk.b, walk.h);
       const bool mine_out = r < walk.nrows;
       const int64_t at = (int64_t)(walk.s.t0 + tok) * (p.G * p.c.Hk) + head;
       const float zero = m - kPBias;
