@@ -7,7 +7,7 @@
 // time.  Per step and tile: S = Q K^T (tcgen05, fp16 x fp16 -> fp32 in TMEM),
 // one thread per row takes the softmax (its 64 logits in registers) and
 // leaves the weights in TMEM over S, O += P V (the weights as the TMEM
-// operand).  Seven further warps turn the codes into fp16 tiles in shared
+// operand).  Six further warps turn the codes into fp16 tiles in shared
 // memory, up to four steps ahead, once for both row tiles.  S is double
 // buffered, so the products of the next step run while a tile's rows are in
 // the softmax.
@@ -38,8 +38,9 @@ constexpr int kChunkGroups = kChunkKeys / 16;  // no page ends inside 16 positio
 constexpr int kChunkSlots = 4;                 // steps of fp16 tiles
 constexpr int kChunkRows = 256;
 constexpr int kSoftWarps = 8;
-constexpr int kConvWarps = 7;  // with the products' 16 warps: 128 registers a thread
-constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kConvWarps = 6;
+constexpr int kMmaWarps = 2;   // one per row tile; 16 warps in all: 128 registers a thread
+constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + kMmaWarps);
 constexpr int kMetaSlots = 8;
 
 template <int D>
@@ -69,7 +70,7 @@ struct ChunkSmem {
   volatile uint32_t abort_flag;
   long long sum[kChunkThreads / 32], tiles[kChunkThreads / 32];
   long long pre;
-  int b;
+  int b, h, x, from;
 };
 
 template <int D>
@@ -258,8 +259,8 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const AttnParams &p, int b) {
 
 __device__ __forceinline__ int chunk_steps(const ChunkSeq &s, int G, int x) {
   const int rows = min((x + 1) * kChunkRows, s.T * G);
-  const int64_t seen = min64((int64_t)s.pos0 + (rows - 1) / G + 1, s.reach);
-  return max(1, (int)((seen + kChunkKeys - 1) / kChunkKeys));
+  const int last = min(s.pos0 + (rows - 1) / G, s.reach - 1);
+  return last < 0 ? 1 : last / kChunkKeys + 1;
 }
 
 struct ChunkWalk {
@@ -270,20 +271,10 @@ struct ChunkWalk {
   int steps, first, last;  // of the tile; the CTA's steps of it are [first, last)
   int row0, nrows, pos_first, pos_last;
 
-  __device__ ChunkWalk(const AttnParams &p_, long long u0_, long long u1_, int b_, long long pre)
-      : p(p_), u(u0_), u1(u1_), b(b_) {
-    s = chunk_seq(p, b);
-    long long per = 0;  // steps of the sequence per kv head
-    for (int i = 0; i < s.tiles; ++i) per += chunk_steps(s, p.G, i);
-    long long r = u - pre;
-    h = (int)(r / per);
-    r -= (long long)h * per;
-    for (x = 0; x < s.tiles - 1; ++x) {
-      const int n = chunk_steps(s, p.G, x);
-      if (r < n) break;
-      r -= n;
-    }
-    set((int)r);
+  __device__ ChunkWalk(const AttnParams &p_, long long u0_, long long u1_, int b_, int h_, int x_,
+                       int from)
+      : p(p_), u(u0_), u1(u1_), s(chunk_seq(p_, b_)), b(b_), h(h_), x(x_) {
+    set(from);
   }
   __device__ void set(int from) {
     steps = chunk_steps(s, p.G, x);
@@ -338,34 +329,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     }
     for (int i = 0; i < kChunkSlots; ++i) {
       mbar_init(&sm.k_full[i], kChunkGroups);
-      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.k_empty[i], kMmaWarps);
       mbar_init(&sm.v_full[i], kChunkGroups);
-      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.v_empty[i], kMmaWarps);
     }
     for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sm.meta_full[i], kChunkGroups);
-    mbar_init(&sm.drained, 1);
+    mbar_init(&sm.drained, kMmaWarps);
     sm.abort_flag = 0u;
-    sm.b = 0;
+    sm.b = sm.h = sm.x = sm.from = 0;
     sm.pre = 0;
     fence_barrier_init();
   }
-  // ---- this CTA's stretch of the line ----
-  long long mine = 0, tiles = 0;
-  for (int b = tid; b < p.s.B; b += kChunkThreads) {
+  // ---- this CTA's stretch of the line.  Steps per sequence and kv head first
+  // (a warp each, a lane per tile), kept where the queries go later ----
+  long long *const per_seq = reinterpret_cast<long long *>(sm.q[0]);
+  static_assert(sizeof(sm.q) >= kMaxSeqs * sizeof(long long), "every sequence's steps");
+  long long tiles = 0;
+  for (int b = warp; b < p.s.B; b += kWarps) {
     const ChunkSeq s = chunk_seq(p, b);
+    int steps = 0;
+    for (int x = lane; x < s.tiles; x += 32) steps += chunk_steps(s, p.G, x);
+    steps = __reduce_add_sync(0xffffffffu, steps);
+    if (lane == 0) {
+      per_seq[b] = steps;
+      if (s.tiles > 0 && blockIdx.x == 0 && p.s.lens[b] > s.reach) raise_status(kStatusBadIndex);
+    }
     tiles += s.tiles;
-    for (int x = 0; x < s.tiles; ++x) mine += chunk_steps(s, p.G, x);
-    if (s.tiles > 0 && blockIdx.x == 0 && p.s.lens[b] > s.reach) raise_status(kStatusBadIndex);
   }
+  if (lane == 0) sm.tiles[warp] = tiles;
+  __syncthreads();
+  long long mine = 0;
+  for (int b = tid; b < p.s.B; b += kChunkThreads) mine += per_seq[b];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-  }
-  if (lane == 0) {
-    sm.sum[warp] = mine;
-    sm.tiles[warp] = tiles;
-  }
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sm.sum[warp] = mine;
   __syncthreads();
   long long W = 0;
   tiles = 0;
@@ -385,12 +382,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   long long before = 0;
   for (int b0 = 0; b0 < p.s.B; b0 += kChunkThreads) {
     const int b = b0 + tid;
-    long long w = 0;
-    if (b < p.s.B) {
-      const ChunkSeq s = chunk_seq(p, b);
-      for (int x = 0; x < s.tiles; ++x) w += chunk_steps(s, p.G, x);
-      w *= p.c.Hk;
-    }
+    const long long w = b < p.s.B ? per_seq[b] * p.c.Hk : 0;
     const long long incl = warp_incl_scan64(w);
     __syncthreads();
     if (lane == 31) sm.sum[warp] = incl;
@@ -407,6 +399,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     }
     if (before > u0) break;  // uniform
   }
+  __syncthreads();
+  if (warp == 0) {  // its kv head and tile
+    const int b = sm.b;
+    const ChunkSeq s = chunk_seq(p, b);
+    const long long per = max(per_seq[b], 1ll);
+    const int h = (int)((u0 - sm.pre) / per);
+    int r = (int)(u0 - sm.pre - h * per);  // steps of that head before u0
+    for (int x0 = 0; x0 < s.tiles; x0 += 32) {
+      const int x = x0 + lane, n = x < s.tiles ? chunk_steps(s, p.G, x) : 0;
+      const int incl = (int)warp_incl_scan((uint32_t)n);
+      const uint32_t who = __ballot_sync(0xffffffffu, r < incl);
+      if (who) {
+        if (lane == __ffs(who) - 1) {
+          sm.h = h;
+          sm.x = x;
+          sm.from = r - (incl - n);
+        }
+        break;
+      }
+      r -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
   if (warp == kWarps - 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sm.tmem_base)),
@@ -418,7 +432,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  ChunkWalk walk(p, u0, u1, sm.b, sm.pre);
+  ChunkWalk walk(p, u0, u1, sm.b, sm.h, sm.x, sm.from);
 
   if (warp < kSoftWarps) {
     // ---------------- softmax: one thread per query row ----------------
@@ -740,63 +754,64 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       if (more) look(there);
     }
   } else if (elect_one()) {
-    // ---------------- products ----------------
+    // ---------------- products: one thread per row tile ----------------
+    // (its waits for weights then never hold up the other tile's products)
+    const int tile = warp - kSoftWarps - kConvWarps;
     constexpr uint32_t kIdQK = chunk_idesc(kChunkKeys, false), kIdPV = chunk_idesc(D, true);
-    uint32_t n_seg[2] = {0u, 0u}, n_s[2] = {0u, 0u}, n_p[2] = {0u, 0u};
+    uint32_t n_seg = 0u, n_s = 0u, n_p = 0u;  // tiles, logits and weights so far
     int k_index = 0;
     bool ok = true;
-    const uint64_t q_desc = chunk_desc(sm.q[0], 16), k_desc = chunk_desc(sm.k[0], 16);
+    const uint64_t q_desc = chunk_desc(sm.q[tile], 16), k_desc = chunk_desc(sm.k[0], 16);
     const uint64_t v_desc = chunk_desc(sm.v[0], S::SUB);
-    auto qk = [&](int tile, int slot) {
-      const uint32_t buf = n_s[tile]++ & 1u;
-      const uint64_t a = q_desc + (uint64_t)(tile * S::DH * S::QSUB >> 4);
+    const uint32_t t_s = tmem + (uint32_t)(tile * 128), t_o = tmem + 256u + (uint32_t)(tile * D);
+    // the logits of step k
+    auto qk = [&](int k) {
+      const int slot = k % kChunkSlots;
+      ok = chunk_wait(sm, &sm.k_full[slot], (uint32_t)(k / kChunkSlots) & 1u);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t buf = n_s++ & 1u;
       const uint64_t b = k_desc + (uint64_t)(slot * S::DH * S::SUB >> 4);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
-        umma_f16_ss(tmem + (uint32_t)(tile * 128) + buf * 64u,
-                    a + (uint64_t)((s >> 2) * S::QSUB >> 4) + 2 * (s & 3),
+        umma_f16_ss(t_s + buf * 64u, q_desc + (uint64_t)((s >> 2) * S::QSUB >> 4) + 2 * (s & 3),
                     b + (uint64_t)((s >> 2) * S::SUB >> 4) + 2 * (s & 3), kIdQK, s > 0 ? 1u : 0u);
       umma_commit(&sm.s_full[tile][buf]);
-    };
-    auto pv = [&](int tile, int slot, uint32_t buf, bool more) {
-      const uint64_t b = v_desc + (uint64_t)(slot * S::DH * S::SUB >> 4);
-#pragma unroll
-      for (int s = 0; s < kChunkKeys / 16; ++s)
-        umma_f16_ts(tmem + 256u + (uint32_t)(tile * D),
-                    tmem + (uint32_t)(tile * 128) + buf * 64u + (uint32_t)(8 * s),
-                    b + (uint64_t)(s * 2048 >> 4), kIdPV, more || s > 0 ? 1u : 0u);
-      umma_commit(&sm.o_done[tile][buf]);
+      umma_commit(&sm.k_empty[slot]);
     };
     do {
       const int n = walk.last - walk.first;
-      const int tiles = walk.nrows > 128 ? 2 : 1;
-      for (int i = 0; i < tiles && ok; ++i) ok = chunk_wait(sm, &sm.q_full[i], n_seg[i]++ & 1u);
+      if (tile * 128 >= walk.nrows) {  // no row of this tile: the slots pass by
+        for (int t = 0; t < n && ok; ++t, ++k_index) {
+          const int slot = k_index % kChunkSlots;
+          const uint32_t phase = (uint32_t)(k_index / kChunkSlots) & 1u;
+          ok = chunk_wait(sm, &sm.k_full[slot], phase);
+          if (ok) mbar_arrive(&sm.k_empty[slot]);
+          ok = ok && chunk_wait(sm, &sm.v_full[slot], phase);
+          if (ok) mbar_arrive(&sm.v_empty[slot]);
+        }
+        continue;
+      }
+      ok = chunk_wait(sm, &sm.q_full[tile], n_seg++ & 1u);
       // logits two steps ahead of the weights: a buffer of S is free again as
       // soon as the product of its weights has been issued
-      auto logits = [&](int i, int at, bool first) {  // step k_index + at of tile i
-        const int k = k_index + at, slot = k % kChunkSlots;
-        if (first) {
-          ok = chunk_wait(sm, &sm.k_full[slot], (uint32_t)(k / kChunkSlots) & 1u);
-          if (!ok) return;
-          tc_fence_after();
-        }
-        qk(i, slot);
-        if (i == tiles - 1) umma_commit(&sm.k_empty[slot]);
-      };
-      for (int at = 0; at < min(n, 2) && ok; ++at)
-        for (int i = 0; i < tiles && ok; ++i) logits(i, at, i == 0);
+      for (int at = 0; at < min(n, 2) && ok; ++at) qk(k_index + at);
       for (int t = 0; t < n && ok; ++t, ++k_index) {
         const int slot = k_index % kChunkSlots;
-        ok = chunk_wait(sm, &sm.v_full[slot], (uint32_t)(k_index / kChunkSlots) & 1u);
-        for (int i = 0; i < tiles && ok; ++i) {
-          const uint32_t buf = n_p[i] & 1u, phase = (n_p[i] >> 1) & 1u;
-          ++n_p[i];
-          if (!(ok = chunk_wait(sm, &sm.p_full[i][buf], phase))) break;
-          tc_fence_after();
-          pv(i, slot, buf, t > 0);
-          if (i == tiles - 1) umma_commit(&sm.v_empty[slot]);
-          if (t + 2 < n) logits(i, 2, i == 0);
-        }
+        const uint32_t buf = n_p & 1u, phase = (n_p >> 1) & 1u;
+        ++n_p;
+        ok = chunk_wait(sm, &sm.v_full[slot], (uint32_t)(k_index / kChunkSlots) & 1u) &&
+             chunk_wait(sm, &sm.p_full[tile][buf], phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b = v_desc + (uint64_t)(slot * S::DH * S::SUB >> 4);
+#pragma unroll
+        for (int s = 0; s < kChunkKeys / 16; ++s)
+          umma_f16_ts(t_o, t_s + buf * 64u + (uint32_t)(8 * s), b + (uint64_t)(s * 2048 >> 4),
+                      kIdPV, t > 0 || s > 0 ? 1u : 0u);
+        umma_commit(&sm.o_done[tile][buf]);
+        umma_commit(&sm.v_empty[slot]);
+        if (t + 2 < n) qk(k_index + 2);
       }
     } while (ok && walk.next());
     // every product done before the tensor memory is freed
