@@ -12,8 +12,8 @@
 // than kSlack, which one vote of the warp finds out; so a row's maximum is
 // seldom reduced and its output seldom rescaled.  The weights are rounded once
 // to fp16, 2^10 at m: 2^-11 of each weight, and weights down to 2^-34 of the
-// largest are not lost.  Sums of weights and outputs stay in fp32; a page's scale multiplies its fp32 partial
-// output, so scales far apart lose nothing.
+// largest are not lost.  Sums of weights and outputs stay in fp32; a page's
+// scale multiplies its fp32 partial output, so scales far apart lose nothing.
 #pragma once
 
 #include <cuda.h>
@@ -49,15 +49,16 @@ __device__ __forceinline__ void tma_load_rows(void *smem, const CUtensorMap *map
 
 // Bounded wait whose polls may suspend the warp, leaving its issue slots to
 // the others of the SM: ~2^32 cycles at most, then recorded (bit 1).
-__device__ __forceinline__ void mbar_wait_suspended(uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
   const long long start = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (clock64() - start > (1ll << 32)) {
       raise_status(kStatusWaitTimeout);
-      return;
+      return false;
     }
   }
+  return true;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -115,8 +116,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // Few query rows per sequence (decode, drafts) or a list of blocks per token:
 // the work is the stream of the cache's bytes.
 //
-// A tile is 4, 8, 16, 24 or 32 query rows (token-major, the group's heads inside) of one
-// sequence and kv head; its keys are cut into units of 32 positions.  The
+// A tile is 4, 8, 16, 24 or 32 query rows (token-major, the group's heads
+// inside) of one sequence and kv head; its keys are cut into units of 32
+// positions.  The
 // units of all tiles form one line, cut evenly over the CTAs (lengths differ
 // by orders of magnitude between sequences), so a CTA works on the end of a
 // tile, whole tiles and the beginning of one; a tile that several CTAs share
@@ -303,7 +305,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
     pre = s_pre;
   }
 
-  int n_issued = 0;  // units issued by this warp so far: stage and phase
+  int n_issued = 0;     // units issued by this warp so far: stage and phase
+  bool broken = false;  // a copy did not arrive: this warp reads no more
   int4 rec = make_int4(-1, 0, 0, 0);
   for (long long u = u0; u < u1;) {
     // ---- the tile that holds unit u ----
@@ -515,16 +518,25 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
         }
       }
     };
-    for (int i = 0; i < min(mine, kStages); ++i) issue(i);
+    for (int i = 0; i < (broken ? 0 : min(mine, kStages)); ++i) issue(i);
 
-    for (int i = 0; i < mine; ++i) {
+    for (int i = 0; i < (broken ? 0 : mine); ++i) {
       if ((i >> 5) != group) {
         cur = nxt;
         ++group;
         load_meta(nxt, group + 1);
       }
       const int st = (base + i) % kStages;
-      mbar_wait_suspended(&s_bar[warp][st], (uint32_t)((base + i) / kStages) & 1u);
+      const bool landed =
+          mbar_wait_suspended(&s_bar[warp][st], (uint32_t)((base + i) / kStages) & 1u);
+      if (!__all_sync(0xffffffffu, landed)) {
+        // given up: no more copies, and those under way get the same chance
+        for (int k = i + 1; k < min(mine, i + kStages); ++k)
+          mbar_wait_suspended(&s_bar[warp][(base + k) % kStages],
+                              (uint32_t)((base + k) / kStages) & 1u);
+        broken = true;
+        break;
+      }
       float ks[2], vs[2];
       int pos[2];
       bool any = false;

@@ -497,6 +497,142 @@ def test_attn_results_do_not_depend_on_the_batch_order_of_runs():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def attn_on_gpu(q, c, table, cu, lens, sm_scale):
+    """tests._kv8.attn in float64 on the GPU, a head at a time, for lengths that
+    the host takes long for; no lists."""
+    P, Hk, bs, D = c["k"].shape
+    n, H = q.shape[:2]
+    G = H // Hk
+    x = {k: dev(v).double() for k, v in c.items() if k in ("k", "v", "k_scale", "v_scale")}
+    qd = dev(q).double()
+    out = torch.zeros((n, H, D), dtype=torch.float64, device="cuda")
+    lse = torch.full((n, H), -np.inf, dtype=torch.float64, device="cuda")
+    A, S = torch.zeros_like(out), torch.zeros_like(lse)
+    N, M = torch.zeros_like(lse), torch.zeros_like(lse)
+    for b, m in enumerate(lens):
+        t0, t1 = int(cu[b]), int(cu[b + 1])
+        if t1 == t0 or m == 0:
+            continue
+        pages = dev(table[b, :cdiv(m, bs)].astype(np.int64))
+        pos = torch.arange(m - (t1 - t0), m, device="cuda")
+        hidden = torch.arange(m, device="cuda")[None] > pos[:, None]
+        for h in range(Hk):
+            k = (x["k"][pages, h] * x["k_scale"][pages, h][:, None, None]).reshape(-1, D)[:m]
+            v = (x["v"][pages, h] * x["v_scale"][pages, h][:, None, None]).reshape(-1, D)[:m]
+            for a in range(h * G, (h + 1) * G):
+                y = (qd[t0:t1, a] @ k.T * sm_scale).masked_fill(hidden, -np.inf)
+                lse[t0:t1, a] = torch.logsumexp(y, -1)
+                w = (y - lse[t0:t1, a][:, None]).exp()
+                out[t0:t1, a] = w @ v
+                A[t0:t1, a] = w @ v.abs()
+                S[t0:t1, a] = (qd[t0:t1, a].abs() @ k.abs().T).amax(-1) * abs(sm_scale)
+                N[t0:t1, a] = (pos + 1).double()
+                M[t0:t1, a] = 127 * x["v_scale"][pages, h].max()
+    return [y.cpu().numpy() for y in (out, lse)] + [[y.cpu().numpy() for y in (A, S, N, M)]]
+
+
+@pytest.mark.parametrize("lens,adds,H,Hk,D,bs", [
+    ([50000, 3000, 1], [1, 1, 1], 16, 2, 128, 64), ([30000, 9000], [1, 1], 4, 1, 64, 16),
+    ([20000], [1], 8, 8, 128, 128), ([25000, 700], [5, 5], 16, 4, 128, 64),
+    ([18000, 18000], [4, 7], 16, 4, 64, 32), ([6000, 4000], [700, 300], 16, 4, 128, 64),
+    ([5000], [1500], 8, 2, 64, 16), ([9000, 100, 3000], [33, 100, 257], 32, 2, 128, 32),
+    ([2500], [2500], 4, 4, 128, 128), ([7000], [900], 12, 4, 64, 64)])
+def test_attn_long(lens, adds, H, Hk, D, bs):
+    rng = np.random.default_rng(sum(lens) + D)
+    table, cu, P = make_step(rng, lens, adds, bs)
+    c = ref.new_cache(rng, P, Hk, bs, D)
+    n = int(cu[-1])
+    q = ref.bf16(rng.standard_normal((n, H, D)).astype(np.float32))
+    g, args = gpu_cache(c), (dev(table), dev(cu), dev(np.int32(lens)))
+    want = attn_on_gpu(q, c, table, cu, lens, D ** -0.5)
+    first = None
+    for _ in range(3):  # the same bits every time
+        out, lse = csa2.kv8_attn(dev_bf16(q), g, *args)
+        check_attn(out, lse, *want, n)
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    if n <= 20:  # every block listed: the same rows through the lists
+        width = max(cdiv(m, bs) for m in lens)
+        sel = np.broadcast_to(np.arange(width, dtype=np.int32), (n, Hk, width))
+        out, lse = csa2.kv8_attn(dev_bf16(q), g, *args, sel=dev(sel))
+        check_attn(out, lse, *want, n)
+    assert csa2.get_device_status() == 0
+
+
+def test_cache_beyond_32_bit_offsets():
+    """Pages whose codes lie past 4 GiB: write, read back, choose, attend."""
+    rng = np.random.default_rng(21)
+    Hk, bs, D, H = 4, 128, 128, 8
+    P = (1 << 32) // (Hk * bs * D) + 12
+    assert (P - 1) * Hk * bs * D > 1 << 32
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB of device memory")
+    g = csa2.KV8Cache(*(torch.empty(s, dtype=d, device="cuda") for s, d in (
+        ((P, Hk, bs, D), torch.int8), ((P, Hk, bs, D), torch.int8), ((P, Hk), torch.float32),
+        ((P, Hk), torch.float32), ((P, Hk, D), torch.int16))))
+    used = np.array([P - 1, 3, P - 2, P - 7, 0, P - 3], np.int32)
+    small = ref.new_cache(rng, len(used), Hk, bs, D)   # those pages alone
+    at = dev(used.astype(np.int64))
+    for name in ("k", "v", "k_scale", "v_scale", "k_sum"):
+        getattr(g, name)[at] = dev(small[name])
+    # three pages for each of two sequences; one decode token and 30 tokens
+    for adds, lens in (([1, 1], [300, 384]), ([30, 30], [330, 380])):
+        cu = np.concatenate([[0], np.cumsum(adds)]).astype(np.int32)
+        n = int(cu[-1])
+        local = np.arange(6, dtype=np.int32).reshape(2, 3)
+        pos = np.concatenate([np.arange(m - a, m) for m, a in zip(lens, adds)])
+        seq = np.repeat([0, 1], adds)
+        slots = local[seq, pos // bs].astype(np.int64) * bs + pos % bs
+        x = ref.bf16(rng.standard_normal((n, H + 2 * Hk, D)).astype(np.float32))
+        ref.append(small, x[:, H:H + Hk], x[:, H + Hk:], slots)
+        far = used[local[seq, pos // bs]].astype(np.int64) * bs + pos % bs
+        xs = dev_bf16(x)
+        csa2.kv8_append(g, xs[:, H:H + Hk], xs[:, H + Hk:], dev(far))
+        for name in ("k_scale", "v_scale", "k_sum", "k", "v"):
+            assert np.array_equal(getattr(g, name)[at].cpu().numpy(), small[name]), name
+        k, v = csa2.kv8_unpack(g, dev(far))
+        assert np.array_equal(k.cpu().numpy(), (
+            small["k"].astype(np.float32) * small["k_scale"][:, :, None, None]).transpose(
+                0, 2, 1, 3).reshape(-1, Hk, D)[slots])
+        args = (dev(used[local]), dev(cu), dev(np.int32(lens)))
+        lists = np.zeros((n, Hk, 2), np.int32)
+        ref.select(x[:, :H], small, local, cu, lens, 2, 0, 1, lists)
+        got = csa2.kv8_select(xs[:, :H], g, *args, 2, 0, 1)
+        assert np.array_equal(got.cpu().numpy(), lists)
+        for sel in (None, lists):
+            out, lse = csa2.kv8_attn(xs[:, :H], g, *args, sel=None if sel is None else got)
+            check_attn(out, lse, *ref.attn(x[:, :H], small, local, cu, lens, sel), n)
+    assert csa2.get_device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls with scratch of their own run side by side; each keeps its bits."""
+    rng = np.random.default_rng(22)
+    jobs = []
+    for lens, adds, H, Hk in (([6000, 900], [1, 1], 16, 2), ([1500], [200], 8, 2),
+                              ([4000, 4000], [5, 5], 16, 4)):
+        table, cu, P = make_step(rng, lens, adds, 32)
+        c = ref.new_cache(rng, P, Hk, 32, 128)
+        q = dev_bf16(ref.bf16(rng.standard_normal((int(cu[-1]), H, 128)).astype(np.float32)))
+        args = (q, gpu_cache(c), dev(table), dev(cu), dev(np.int32(lens)))
+        sel = csa2.kv8_select(*args, 6)
+        jobs.append((args, sel, csa2.kv8_attn(*args), csa2.kv8_attn(*args, sel=sel)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(8):
+        for (args, sel, _, _), st, res in zip(jobs, streams, got):
+            with torch.cuda.stream(st):
+                s = csa2.kv8_select(*args, 6)
+                res.append((s, csa2.kv8_attn(*args), csa2.kv8_attn(*args, sel=s)))
+    torch.cuda.synchronize()
+    for (args, sel, dense, listed), res in zip(jobs, got):
+        for s, a, b in res:
+            assert torch.equal(s, sel)
+            assert all(torch.equal(x, y) for x, y in zip(a + b, dense + listed))
+    assert csa2.get_device_status() == 0
+
+
 # --- together -----------------------------------------------------------------
 
 def test_a_serving_run_prompt_decode_drafts_then_a_captured_step():
