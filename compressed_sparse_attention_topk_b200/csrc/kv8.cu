@@ -150,34 +150,54 @@ csa2_status launch_select(const kv8::SelectParams &p, cudaStream_t st) {
                           staged ? size_t(p.s.width) * 4 : 0, st, p, staged);
 }
 
-// The kernel of an attention call and its workspace.
-struct AttnPlan {
-  bool chunk;      // 256-row tiles on tcgen05
-  int rows;        // else: query rows in a tile
+// One attention kernel of a call and its workspace.
+struct AttnPart {
+  int rows;        // query rows in a tile (0: the kernel is not used)
   int ctas;
-  size_t part_at;  // the partials, behind one record per CTA
+  size_t rec_at, part_at;  // one record per CTA, and the partials
+};
+
+struct AttnPlan {
+  AttnPart split, chunk;  // the split stream; 256-row tiles on tcgen05
   size_t bytes;
 };
 
-// As many query rows in a tile as a sequence (or, with lists, a token) has on
-// average, up to 32: every row of a tile reads the same fragments of the
-// cache.  More rows than that go to the tensor-core tiles.
+// Sequences of up to 32 query rows (tokens x heads of a group) belong to the
+// split stream, with as many rows in a tile as they have -- every row of a
+// tile reads the same fragments of the cache -- and longer ones to the
+// tensor-core tiles.  The host knows the numbers of tokens and sequences only.
+// Where one of several sequences may have a tile's 256 rows beyond a token for
+// each, both kernels run, each on its own sequences (31 decode tokens of
+// 32,768 positions and 512 tokens of 16,384 in one step: 320 us instead of 760;
+// a kernel that finds no sequence costs about 4 us); else the average decides.
+// The split stream's tile is then the average, or a decode token's group where
+// the tokens cannot be the same for all.  With lists everything is the split
+// stream's, by the heads of a group.
+constexpr int64_t kSplitRows = 32;
+
 AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
   AttnPlan a{};
   const int64_t rows = n_sel > 0 ? G : ceil_div(n * G, std::max(B, 1));
-  a.chunk = n_sel == 0 && rows > 32;
-  a.rows = rows <= 4 ? 4 : 8 * (int)std::min<int64_t>(4, ceil_div(rows, 8));
-  a.ctas = (a.chunk ? 1 : a.rows <= 8 ? 3 : 2) * device_sms();
-  a.part_at = align_up(size_t(a.ctas) * sizeof(int4), 256);
-  const size_t tile_rows = a.chunk ? kv8::kChunkRows : a.rows;
-  a.bytes = a.part_at + align_up(size_t(a.ctas) * 2 * tile_rows * (D + 2) * 4, 256);
+  const bool mixed = n_sel == 0 && B > 1 && (n - B) * G >= kv8::kChunkRows;
+  auto tile = [](int64_t r) { return r <= 4 ? 4 : 8 * (int)std::min<int64_t>(4, ceil_div(r, 8)); };
+  if (mixed) a.split.rows = tile(n % B == 0 && rows <= kSplitRows ? rows : G);
+  else if (n_sel > 0 || rows <= kSplitRows) a.split.rows = tile(rows);
+  if (mixed || (n_sel == 0 && rows > kSplitRows)) a.chunk.rows = kv8::kChunkRows;
+  a.split.ctas = (a.split.rows <= 8 ? 3 : 2) * device_sms();
+  a.chunk.ctas = device_sms();
+  for (AttnPart *part : {&a.split, &a.chunk}) {
+    if (!part->rows) continue;
+    part->rec_at = a.bytes;
+    part->part_at = part->rec_at + align_up(size_t(part->ctas) * sizeof(int4), 256);
+    a.bytes = part->part_at + align_up(size_t(part->ctas) * 2 * part->rows * (D + 2) * 4, 256);
+  }
   return a;
 }
 
 // Merges the tiles that several CTAs shared; its blocks come up while the
 // attention kernel's last ones run.
 template <int D, int ROWS, int RPB>
-csa2_status launch_merge(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+csa2_status launch_merge(const kv8::AttnParams &p, const AttnPart &a, cudaStream_t st) {
   TraceScope ts("kv8_attn_merge", st);
   return launch_dependent(kv8::kv8_merge_kernel<D, ROWS, RPB>,
                           dim3((unsigned)a.ctas, ROWS / RPB), kv8::kMergeThreads, 0, st, p,
@@ -185,7 +205,7 @@ csa2_status launch_merge(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
 }
 
 template <int D>
-csa2_status launch_chunk(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+csa2_status launch_chunk(const kv8::AttnParams &p, const AttnPart &a, cudaStream_t st) {
   const size_t smem = kv8::chunk_smem_bytes<D>();
   static std::atomic<bool> done[256];  // per device: attributes set
   int dev = 0;
@@ -204,7 +224,7 @@ csa2_status launch_chunk(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
 }
 
 template <int D, int ROWS, bool P16>
-csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+csa2_status launch_split(const kv8::AttnParams &p, const AttnPart &a, cudaStream_t st) {
   using S = kv8::SplitShape<D, ROWS>;
   static std::atomic<bool> done[256];  // per device: attributes set
   int dev = 0;
@@ -236,7 +256,7 @@ csa2_status launch_split(const kv8::AttnParams &p, const AttnPlan &a, cudaStream
 }
 
 template <int D, bool P16>
-csa2_status launch_attn_d(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
+csa2_status launch_split_rows(const kv8::AttnParams &p, const AttnPart &a, cudaStream_t st) {
   switch (a.rows) {
     case 4: return launch_split<D, 4, P16>(p, a, st);
     case 8: return launch_split<D, 8, P16>(p, a, st);
@@ -246,11 +266,23 @@ csa2_status launch_attn_d(const kv8::AttnParams &p, const AttnPlan &a, cudaStrea
   }
 }
 
-csa2_status launch_attn(const kv8::AttnParams &p, const AttnPlan &a, cudaStream_t st) {
-  if (a.chunk) return p.c.D == 64 ? launch_chunk<64>(p, a, st) : launch_chunk<128>(p, a, st);
+csa2_status launch_attn(kv8::AttnParams p, const AttnPlan &a, char *ws, cudaStream_t st) {
+  const bool both = a.split.rows && a.chunk.rows;
+  p.split_rows = both ? (int32_t)kSplitRows : 0;
+  if (a.chunk.rows) {
+    p.rec = reinterpret_cast<int4 *>(ws + a.chunk.rec_at);
+    p.part = reinterpret_cast<float *>(ws + a.chunk.part_at);
+    const csa2_status rc = p.c.D == 64 ? launch_chunk<64>(p, a.chunk, st)
+                                       : launch_chunk<128>(p, a.chunk, st);
+    if (rc != CSA2_OK || !both) return rc;
+  }
+  p.rec = reinterpret_cast<int4 *>(ws + a.split.rec_at);
+  p.part = reinterpret_cast<float *>(ws + a.split.part_at);
   if (p.c.bs == 16)
-    return p.c.D == 64 ? launch_attn_d<64, true>(p, a, st) : launch_attn_d<128, true>(p, a, st);
-  return p.c.D == 64 ? launch_attn_d<64, false>(p, a, st) : launch_attn_d<128, false>(p, a, st);
+    return p.c.D == 64 ? launch_split_rows<64, true>(p, a.split, st)
+                       : launch_split_rows<128, true>(p, a.split, st);
+  return p.c.D == 64 ? launch_split_rows<64, false>(p, a.split, st)
+                     : launch_split_rows<128, false>(p, a.split, st);
 }
 
 }  // namespace
@@ -407,9 +439,7 @@ csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *c
   p.out = out;
   p.lse = lse;
   const AttnPlan plan = attn_plan(n, B, p.G, p.c.D, n_sel);
-  p.rec = static_cast<int4 *>(ws);
-  p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + plan.part_at);
-  return launch_attn(p, plan, as_stream(stream));
+  return launch_attn(p, plan, static_cast<char *>(ws), as_stream(stream));
 }
 
 }  // extern "C"

@@ -36,6 +36,8 @@ struct AttnParams {
   float *lse;           // [n, H] or null
   float *part;          // split tiles: partial results, two per CTA
   int4 *rec;            // split tiles: one record per CTA
+  int32_t split_rows;   // > 0: sequences of more rows are kv8_chunk_kernel's, the others
+                        // kv8_split_kernel's; 0: the kernel serves them all
 };
 
 __device__ __forceinline__ void tma_load_rows(void *smem, const CUtensorMap *map, int row,
@@ -178,7 +180,8 @@ __device__ __forceinline__ void seq_work(const AttnParams &p, int b, int &tiles,
   T = (int)max((int64_t)0, min64(hi, p.s.n) - lo);
   const int64_t len = p.s.lens[b];
   pos0 = (int)max((int64_t)-0x40000000, len - hi + lo);
-  tiles = (int)(((int64_t)T * p.G + ROWS - 1) / ROWS);
+  const int64_t rows = (int64_t)T * p.G;
+  tiles = p.split_rows && rows > p.split_rows ? 0 : (int)((rows + ROWS - 1) / ROWS);
   const int64_t reach = (int64_t)p.s.width << p.c.bs_shift;
   const int64_t seen = min64(max(len, (int64_t)0), reach);
   units = max(1, (int)((seen + kUnit - 1) / kUnit));

@@ -252,7 +252,8 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const AttnParams &p, int b) {
   s.t0 = lo;
   s.T = (int)max((int64_t)0, min64(hi, p.s.n) - lo);
   s.pos0 = (int)max((int64_t)-0x40000000, (int64_t)p.s.lens[b] - hi + lo);
-  s.tiles = (int)(((int64_t)s.T * p.G + kChunkRows - 1) / kChunkRows);
+  const int64_t rows = (int64_t)s.T * p.G;
+  s.tiles = rows <= p.split_rows ? 0 : (int)((rows + kChunkRows - 1) / kChunkRows);
   s.reach = p.s.width << p.c.bs_shift;
   return s;
 }

@@ -322,6 +322,10 @@ SHAPES = [
     ([200], [200], 4, 2, 64, 64), ([500, 40], [129, 40], 8, 2, 128, 32),
     ([1300], [300], 16, 4, 128, 64), ([150, 600, 20], [150, 77, 1], 4, 4, 64, 128),
     ([130], [130], 16, 1, 128, 16), ([257], [100], 5, 1, 128, 64), ([90, 35], [64, 33], 24, 8, 64, 16),
+    # long and short sequences in one step: each its own kernel
+    ([700, 300, 40, 9, 1200], [90, 1, 1, 0, 1], 16, 4, 128, 64),
+    ([33, 800, 260], [1, 200, 6], 8, 2, 64, 16), ([400, 64, 700, 5], [1, 64, 8, 2], 16, 2, 128, 32),
+    ([50, 60], [8, 9], 8, 2, 64, 64), ([300, 500, 100], [32, 33, 2], 3, 3, 128, 128),
 ]
 
 
@@ -536,7 +540,8 @@ def attn_on_gpu(q, c, table, cu, lens, sm_scale):
     ([20000], [1], 8, 8, 128, 128), ([25000, 700], [5, 5], 16, 4, 128, 64),
     ([18000, 18000], [4, 7], 16, 4, 64, 32), ([6000, 4000], [700, 300], 16, 4, 128, 64),
     ([5000], [1500], 8, 2, 64, 16), ([9000, 100, 3000], [33, 100, 257], 32, 2, 128, 32),
-    ([2500], [2500], 4, 4, 128, 128), ([7000], [900], 12, 4, 64, 64)])
+    ([2500], [2500], 4, 4, 128, 128), ([7000], [900], 12, 4, 64, 64),
+    ([20000, 9000, 3000, 40], [1, 500, 1, 40], 16, 4, 128, 64)])
 def test_attn_long(lens, adds, H, Hk, D, bs):
     rng = np.random.default_rng(sum(lens) + D)
     table, cu, P = make_step(rng, lens, adds, bs)
