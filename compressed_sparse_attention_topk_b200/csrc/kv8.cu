@@ -169,16 +169,20 @@ struct AttnPlan {
 // Where one of several sequences may have a tile's 256 rows beyond a token for
 // each, both kernels run, each on its own sequences (31 decode tokens of
 // 32,768 positions and 512 tokens of 16,384 in one step: 320 us instead of 760;
-// a kernel that finds no sequence costs about 4 us); else the average decides.
+// a kernel that finds no sequence costs about 8 us, so not where the tables
+// reach fewer than 2^17 positions and kv heads in all: what one kernel loses
+// there is of that size); else the average decides.
 // The split stream's tile is then the average, or a decode token's group where
 // the tokens cannot be the same for all.  With lists everything is the split
 // stream's, by the heads of a group.
 constexpr int64_t kSplitRows = 32;
 
-AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel) {
+constexpr int64_t kBothReach = int64_t(1) << 17;
+
+AttnPlan attn_plan(int64_t n, int32_t B, int32_t G, int32_t D, int32_t n_sel, bool far) {
   AttnPlan a{};
   const int64_t rows = n_sel > 0 ? G : ceil_div(n * G, std::max(B, 1));
-  const bool mixed = n_sel == 0 && B > 1 && (n - B) * G >= kv8::kChunkRows;
+  const bool mixed = far && n_sel == 0 && B > 1 && (n - B) * G >= kv8::kChunkRows;
   auto tile = [](int64_t r) { return r <= 4 ? 4 : 8 * (int)std::min<int64_t>(4, ceil_div(r, 8)); };
   if (mixed) a.split.rows = tile(n % B == 0 && rows <= kSplitRows ? rows : G);
   else if (n_sel > 0 || rows <= kSplitRows) a.split.rows = tile(rows);
@@ -405,7 +409,8 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
                                     int32_t n_sel) {
   if (n < 0 || B < 0 || H < 1 || Hk < 1 || H % Hk != 0 || (D != 64 && D != 128) || n_sel < 0)
     return 0;
-  return attn_plan(n, B, H / Hk, D, n_sel).bytes;
+  return std::max(attn_plan(n, B, H / Hk, D, n_sel, false).bytes,
+                  attn_plan(n, B, H / Hk, D, n_sel, true).bytes);
 }
 
 csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
@@ -438,7 +443,8 @@ csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *c
   p.sm_scale = sm_scale;
   p.out = out;
   p.lse = lse;
-  const AttnPlan plan = attn_plan(n, B, p.G, p.c.D, n_sel);
+  const bool far = int64_t(B) * width * p.c.bs * p.c.Hk >= kBothReach;
+  const AttnPlan plan = attn_plan(n, B, p.G, p.c.D, n_sel, far);
   return launch_attn(p, plan, static_cast<char *>(ws), as_stream(stream));
 }
 

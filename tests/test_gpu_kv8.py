@@ -275,9 +275,10 @@ def test_select_extreme_sums_and_a_bad_page():
 
 # --- attention ----------------------------------------------------------------
 
-def run_attn(rng, lens, adds, H, Hk, D, bs, sel=None, pad=0, edit=None, sm_scale=None, peak=1.0):
+def run_attn(rng, lens, adds, H, Hk, D, bs, sel=None, pad=0, edit=None, sm_scale=None, peak=1.0,
+             extra_width=1):
     """sel: None, or a function (rng, n, Hk, blocks of each token) -> lists."""
-    table, cu, P = make_step(rng, lens, adds, bs)
+    table, cu, P = make_step(rng, lens, adds, bs, extra_width=extra_width)
     c = ref.new_cache(rng, P, Hk, bs, D)
     n = int(cu[-1]) + pad
     q = ref.bf16((peak * rng.standard_normal((n, H + 1, D))).astype(np.float32))
@@ -322,7 +323,7 @@ SHAPES = [
     ([200], [200], 4, 2, 64, 64), ([500, 40], [129, 40], 8, 2, 128, 32),
     ([1300], [300], 16, 4, 128, 64), ([150, 600, 20], [150, 77, 1], 4, 4, 64, 128),
     ([130], [130], 16, 1, 128, 16), ([257], [100], 5, 1, 128, 64), ([90, 35], [64, 33], 24, 8, 64, 16),
-    # long and short sequences in one step: each its own kernel
+    # long and short sequences in one step
     ([700, 300, 40, 9, 1200], [90, 1, 1, 0, 1], 16, 4, 128, 64),
     ([33, 800, 260], [1, 200, 6], 8, 2, 64, 16), ([400, 64, 700, 5], [1, 64, 8, 2], 16, 2, 128, 32),
     ([50, 60], [8, 9], 8, 2, 64, 64), ([300, 500, 100], [32, 33, 2], 3, 3, 128, 128),
@@ -332,6 +333,18 @@ SHAPES = [
 @pytest.mark.parametrize("lens,adds,H,Hk,D,bs", SHAPES)
 def test_attn_all_blocks(lens, adds, H, Hk, D, bs):
     run_attn(np.random.default_rng(sum(lens) + H), lens, adds, H, Hk, D, bs, pad=2)
+    assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,adds,H,Hk,D,bs", [
+    ([700, 300, 40, 9, 1200], [90, 1, 1, 0, 1], 16, 4, 128, 64),
+    ([33, 800, 260], [1, 200, 6], 8, 2, 64, 16), ([400, 64, 700, 5], [1, 64, 8, 2], 16, 2, 128, 32),
+    ([300, 500, 100], [32, 133, 2], 3, 3, 128, 128), ([900, 50, 0], [300, 50, 0], 4, 2, 64, 64),
+    ([64, 64, 64, 64], [33, 32, 31, 64], 8, 8, 128, 32), ([1, 2, 2000], [1, 2, 600], 32, 1, 64, 32)])
+def test_attn_long_and_short_sequences_under_a_wide_table(lens, adds, H, Hk, D, bs):
+    """Tables that reach far: both attention kernels, each on its own sequences."""
+    run_attn(np.random.default_rng(sum(lens) + D), lens, adds, H, Hk, D, bs, pad=3,
+             extra_width=(1 << 17) // bs)
     assert csa2.get_device_status() == 0
 
 
