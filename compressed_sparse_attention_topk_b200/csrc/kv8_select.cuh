@@ -12,7 +12,9 @@
 // for a chunk.  kv8_pick_*_kernel then takes each row's n_sel best: a score is
 // ordered as an unsigned key, forced blocks get the largest key, and the
 // n_sel-th largest key is found by bisection within a warp (rows of up to
-// 2,048 blocks) or by digits over a CTA.  Both latency-bound.
+// 2,048 blocks) or by digits over a CTA.  One token over 4,096 blocks is bound
+// by latency (10 and 9 us); 4,096 tokens over 1,024 blocks and 4 heads by
+// instructions (50 and 40 us).
 #pragma once
 
 #include "kv8_cache.cuh"
