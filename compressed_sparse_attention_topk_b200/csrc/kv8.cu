@@ -299,7 +299,8 @@ csa2_status csa2_block_tables(const int32_t *lens, const int32_t *add, int32_t B
                               int32_t *pos, int64_t cap, int32_t *used, void *stream) {
   if (B < 0 || width < 1 || n_free < 0 || cap < 0 || block < 1) return CSA2_ERR_INVALID_ARG;
   if (!cu || !used || (B > 0 && (!lens || !add || !table || !lens_out)) ||
-      (n_free > 0 && !free_pages) || (cap > 0 && (!slots || !pos)) || (B > 0 && lens_out == lens) ||
+      (n_free > 0 && !free_pages) || (cap > 0 && (!slots || !pos)) ||
+      (B > 0 && (lens_out == lens || lens_out == add)) ||
       !aligned(lens, 4) || !aligned(add, 4) || !aligned(table, 4) || !aligned(free_pages, 4) ||
       !aligned(lens_out, 4) || !aligned(cu, 4) || !aligned(used, 4) || !aligned(slots, 8) ||
       !aligned(pos, 4))

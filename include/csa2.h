@@ -479,7 +479,7 @@ typedef struct csa2_kv8 {
  *               recorded in the device status word, bit 2)
  *   table       device, int32 [B, width]: the new pages' entries are written
  *   free_pages  device, int32 [n_free]
- *   lens_out    device, int32 [B]     lens + add (must not be lens itself)
+ *   lens_out    device, int32 [B]     lens + add (not lens or add itself)
  *   cu          device, int32 [B+1]   token offsets of the requests
  *   slots       device, int64 [cap]   page * block + row of every token of the
  *               step, in request order; -1 from the last token on
@@ -535,7 +535,7 @@ size_t csa2_kv8_select_workspace_size(int64_t n, int32_t Hk, int32_t width);
  * A block whose page is outside the cache scores lowest of all.
  * Supported: H a multiple of Hk, H <= 128, 1 <= n_sel <= 4096, n_first >= 0,
  * n_last >= 1 (the block being filled is always kept), n_first + n_last <=
- * n_sel, width <= 65536, B <= 4096. */
+ * n_sel, width <= 65536, B <= 4096, n * Hk < 2^31. */
 csa2_status csa2_kv8_select(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
                             const int32_t *table, int32_t width, const int32_t *cu,
                             const int32_t *lens, int32_t B, int64_t n, int32_t H, int32_t n_sel,
@@ -553,6 +553,8 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
  * listed blocks -- of values code * scale.  out = sum p * value rounded to
  * bf16 once, lse = natural log of sum exp(logit).  A token that sees nothing
  * (no position, an empty list, only skipped pages) gets out = 0, lse = -inf.
+ * Where a sequence has more than 32 query rows (tokens times H / Hk) a value
+ * scale below 2^-80 of the largest of its pages may count as 0.
  * A sequence with more new tokens than lens has tokens at negative positions,
  * which see nothing.
  *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
@@ -561,8 +563,8 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
  *   out  device, bf16 [n, H, D] (16-byte aligned); lse device, fp32 [n, H] or
  *        NULL
  *   ws   device workspace of ws_bytes >= csa2_kv8_attn_workspace_size
- * Supported: H a multiple of Hk, H <= 128, n_sel <= 65536, B <= 4096,
- * sm_scale finite. */
+ * Supported: H a multiple of Hk, H <= 128, n * H < 2^31, n_sel <= 65536,
+ * B <= 4096, width * block <= 2^30, sm_scale finite. */
 csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,
                           const int32_t *table, int32_t width, const int32_t *cu,
                           const int32_t *lens, int32_t B, int64_t n, int32_t H,

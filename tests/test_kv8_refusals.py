@@ -59,6 +59,7 @@ def tables(lib, **kw):
     (dict(free=None), INVALID), (dict(lens_out=None), INVALID), (dict(cu=None), INVALID),
     (dict(slots=None), INVALID), (dict(pos=None), INVALID), (dict(used=None), INVALID),
     (dict(lens_out=FAKE), INVALID),          # in place: other CTAs still read lens
+    (dict(lens_out=P(512)), INVALID),        # or add
     (dict(slots=P(260)), INVALID), (dict(B=-1), INVALID), (dict(width=0), INVALID),
     (dict(cap=-1), INVALID), (dict(n_free=-1), INVALID), (dict(block=0), INVALID),
     (dict(block=24), UNSUPPORTED), (dict(B=4097), UNSUPPORTED),
@@ -123,7 +124,8 @@ def attn(lib, **kw):
     (dict(sel=FAKE), INVALID), (dict(n_sel=4), INVALID), (dict(sel=P(258), n_sel=4), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(H=130, stride=1 << 16), UNSUPPORTED), (dict(sel=FAKE, n_sel=65537), UNSUPPORTED),
-    (dict(B=4097), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=P(264)), WORKSPACE),
+    (dict(B=4097), UNSUPPORTED), (dict(width=(1 << 24) + 1), UNSUPPORTED),
+    (dict(ws=None), WORKSPACE), (dict(ws=P(264)), WORKSPACE),
     (dict(bytes=8), WORKSPACE)])
 def test_attn_refuses(lib, kw, rc):
     assert attn(lib, **kw) == rc
