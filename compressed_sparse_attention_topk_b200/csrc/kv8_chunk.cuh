@@ -15,8 +15,9 @@
 // The products are exact (codes and power-of-two scaled queries are fp16),
 // sums fp32.  A page's value scale joins its logits instead of its values:
 //   y_j = x_j + log2(vs / vref),  P_j = 2^(y_j - m),  m >= max y - kSlack,
-// so P_j vcode_j vref is p_j vs vcode_j in the row's own units, whatever the
-// scales; the softmax sum takes P_j (vref / vs) page by page.  P is rounded
+// so P_j vcode_j vref is p_j vs vcode_j in the row's own units; the softmax
+// sum takes P_j (vref / vs) page by page.  vref is the largest scale of the
+// sequence's pages; one below 2^-80 of it counts as 0.  P is rounded
 // once to fp16, 2^kPBias at m: 2^-11 of a weight, down to 2^-34 of the
 // largest.  m follows the running maximum only when that has grown by more
 // than kSlack, so O is rarely rescaled.
@@ -45,6 +46,7 @@ constexpr int kConvWarps = 6;
 constexpr int kMmaWarps = 2;   // one per row tile; 16 warps in all: 128 registers a thread
 constexpr int kChunkThreads = 32 * (kSoftWarps + kConvWarps + kMmaWarps);
 constexpr int kMetaSlots = 8;
+constexpr float kLvsFloor = -80.f;  // log2 of the smallest value scale that counts
 
 template <int D>
 struct ChunkShape {
@@ -306,11 +308,32 @@ struct ChunkWalk {
   }
 };
 
-// The unit of a sequence's values: the value scale of its first page.
+// The unit of a sequence's values: the largest value scale of its pages (of a
+// kv head), found by each warp that needs it.  lvs is then at most 0, and the
+// sums of weights keep fp32's range down to kLvsFloor below it: a weight whose
+// P underflows (2^-126) adds less than 2^(-126 + 80) to a sum of at least 2^5.
+// (a call: inlined at its three places it costs the kernel registers)
+__device__ __noinline__ float chunk_top(const int32_t *row, int n, const float *scale, int Hk,
+                                        int pages) {
+  float top = 0.f;
+  for (int j0 = threadIdx.x & 31; j0 < n; j0 += 4 * 32) {
+    int page[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) page[e] = j0 + 32 * e < n ? row[j0 + 32 * e] : -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = page[e] >= 0 && page[e] < pages ? scale[page[e] * Hk] : 0.f;
+      top = v < INFINITY ? fmaxf(top, v) : top;
+    }
+  }
+  top = warp_max(top);
+  return top > 0.f ? top : 1.f;
+}
 __device__ __forceinline__ float chunk_vref(const AttnParams &p, int b, int h) {
-  const int page = p.s.table[(int64_t)b * p.s.width];
-  const float v = page >= 0 && page < p.c.pages ? p.c.v_scale[page * p.c.Hk + h] : 1.f;
-  return v > 0.f && v < INFINITY ? v : 1.f;
+  const int64_t len = max(p.s.lens[b], 0);
+  return chunk_top(p.s.table + (int64_t)b * p.s.width,
+                   (int)min64((len + p.c.bs - 1) >> p.c.bs_shift, p.s.width), p.c.v_scale + h,
+                   p.c.Hk, p.c.pages);
 }
 
 template <int D>
@@ -582,7 +605,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const int64_t at = (int64_t)(walk.s.t0 + tok) * (p.G * p.c.Hk) + head;
       const float zero = m - kPBias;
       float *part = p.part + (2 * c + (walk.first > 0 ? 0 : 1)) * S::PART;
-      const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref;
+      // (a partial is kept in units 2^24 larger: O vref stays in range)
+      const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref * 0x1p-24f;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t v[32];
@@ -622,8 +646,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       if (mine_out && whole && p.lse)
         p.lse[at] = l == 0.f ? -INFINITY : fmaf(zero, 0.693147180559945309417f, logf(l));
       if (mine_out && !whole) {
-        part[kChunkRows * D + r] = l == 0.f ? -INFINITY : zero;
-        part[kChunkRows * D + kChunkRows + r] = l;
+        part[kChunkRows * D + r] = l == 0.f ? -INFINITY : zero + 24.f;
+        part[kChunkRows * D + kChunkRows + r] = l * 0x1p-24f;
       }
       if (!whole && tile == 0) {
         if (walk.first > 0) {
@@ -733,7 +757,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
           !chunk_wait(sm, vals ? &sm.v_empty[slot] : &sm.k_empty[slot],
                       (uint32_t)(here.step / kChunkSlots - 1) & 1u))
         break;
-      const bool zero = vs == 0.f;
+      // (a page without values must not raise the maximum: it takes the floor)
+      const float lvs = vs > 0.f ? log2f(vs) - log2f(here.vref) : vs == 0.f ? -INFINITY : NAN;
+      const bool zero = lvs < kLvsFloor;
       store(vals ? sm.v[slot] : sm.k[slot], cw * 16, vals && zero);
       fence_proxy_async_smem();
       __syncwarp();
@@ -742,8 +768,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         if (!vals) {  // (the softmax is never a ring of these behind)
           const int at = here.step % kMetaSlots;
           sm.meta[at].ks[cw] = ks;
-          sm.meta[at].lvs[cw] = ph < 0 ? -INFINITY : zero ? 0.f : log2f(vs / here.vref);
-          sm.meta[at].ivs[cw] = ph < 0 ? 0.f : zero ? 1.f : here.vref / vs;
+          sm.meta[at].lvs[cw] = ph < 0 ? -INFINITY : zero ? kLvsFloor : lvs;
+          sm.meta[at].ivs[cw] = ph < 0 ? 0.f : zero ? 0x1p80f : here.vref / vs;
           mbar_arrive(&sm.meta_full[at]);
         }
       }

@@ -422,13 +422,17 @@ def test_attn_peaked_flat_and_scaled_logits(T, peak, sm_scale):
 
 
 @pytest.mark.parametrize("T", [1, 70])
-def test_attn_scales_far_apart(T):
-    """Pages of zeros, tiny and large value scales beside one another."""
+@pytest.mark.parametrize("first", [None, 1e-39, 1e30])
+def test_attn_scales_far_apart(T, first):
+    """Pages of zeros, tiny and large value scales beside one another; a first
+    page whose scale is far from all others."""
     def edit(c, table, q):
         c["v_scale"][:] = np.float32(10.0) ** np.random.default_rng(1).integers(
             -9, 4, c["v_scale"].shape).astype(np.float32)
         c["v_scale"][::3] = 0.0
         c["k_scale"][::4] = 0.0
+        if first is not None:
+            c["v_scale"][table[:, 0]] = np.float32(first)
 
     run_attn(np.random.default_rng(13), [600, 200], [T, 1], 8, 2, 64, 16, edit=edit)
     assert csa2.get_device_status() == 0
@@ -463,16 +467,18 @@ def test_attn_rows_of_unwritten_pages_do_not_leak():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_attn_non_finite_queries_stay_in_their_rows():
+@pytest.mark.parametrize("T", [2, 3, 90])
+@pytest.mark.parametrize("H", [4, 8])
+def test_attn_non_finite_queries_stay_in_their_rows(T, H):
     rng = np.random.default_rng(16)
-    table, cu, P = make_step(rng, [200], [3], 64)
+    table, cu, P = make_step(rng, [200], [T], 64)
     c = ref.new_cache(rng, P, 2, 64, 128)
-    q = ref.bf16(rng.standard_normal((3, 8, 128)).astype(np.float32))
+    q = ref.bf16(rng.standard_normal((T, H, 128)).astype(np.float32))
     args = (gpu_cache(c), dev(table), dev(cu), dev(np.int32([200])))
     a = csa2.kv8_attn(dev_bf16(q), *args)[0]
     q[1, 2, 5], q[1, 3, 5] = np.nan, np.inf
     b = csa2.kv8_attn(dev_bf16(q), *args)[0]
-    ok = torch.ones(3, 8, dtype=torch.bool)
+    ok = torch.ones(T, H, dtype=torch.bool)
     ok[1, 2:4] = False
     assert torch.equal(a[ok], b[ok])
     assert b[1, 2].isnan().all()
