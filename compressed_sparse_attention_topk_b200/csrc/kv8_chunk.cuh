@@ -57,9 +57,9 @@ struct ChunkShape {
 };
 
 // Scales of a step's groups of 16 positions: keys; values as log2(vs / vref)
-// and vref / vs.
+// and vref / vs; vref.
 struct ChunkMeta {
-  float ks[kChunkGroups], lvs[kChunkGroups], ivs[kChunkGroups];
+  float ks[kChunkGroups], lvs[kChunkGroups], ivs[kChunkGroups], vref;
 };
 
 template <int D>
@@ -309,10 +309,10 @@ struct ChunkWalk {
 };
 
 // The unit of a sequence's values: the largest value scale of its pages (of a
-// kv head), found by each warp that needs it.  lvs is then at most 0, and the
+// kv head), found by each converter warp.  lvs is then at most 0, and the
 // sums of weights keep fp32's range down to kLvsFloor below it: a weight whose
 // P underflows (2^-126) adds less than 2^(-126 + 80) to a sum of at least 2^5.
-// (a call: inlined at its three places it costs the kernel registers)
+// (a call: inlined at its places it costs the kernel registers)
 __device__ __noinline__ float chunk_top(const int32_t *row, int n, const float *scale, int Hk,
                                         int pages) {
   float top = 0.f;
@@ -481,7 +481,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const int tok = R / p.G;
       const int64_t head = (int64_t)walk.h * p.G + R - tok * p.G;
       const int my_pos = min(walk.s.pos0 + tok, kNoPos - 1);
-      const float vref = chunk_vref(p, walk.b, walk.h);
       float f;  // logit per product, without the page's key scale
       {
         const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -606,6 +605,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const float zero = m - kPBias;
       float *part = p.part + (2 * c + (walk.first > 0 ? 0 : 1)) * S::PART;
       // (a partial is kept in units 2^24 larger: O vref stays in range)
+      const float vref = sm.meta[(k_index - 1) % kMetaSlots].vref;  // (not written again yet)
       const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref * 0x1p-24f;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -700,9 +700,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       part -= 2 * kChunkGroups;
       ++step;
       if (++t < walk.last) return true;
+      const int b = walk.b, h = walk.h;
       if (!walk.next()) return false;
       t = walk.first;
-      vref_now = chunk_vref(p, walk.b, walk.h);
+      if (walk.b != b || walk.h != h) vref_now = chunk_vref(p, walk.b, walk.h);
       return true;
     };
     // page and head, or -1 where nothing is seen or the page is not the cache's
@@ -758,8 +759,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
                       (uint32_t)(here.step / kChunkSlots - 1) & 1u))
         break;
       // (a page without values must not raise the maximum: it takes the floor)
-      const float lvs = vs > 0.f ? log2f(vs) - log2f(here.vref) : vs == 0.f ? -INFINITY : NAN;
-      const bool zero = lvs < kLvsFloor;
+      const bool zero = vs == 0.f || vs < here.vref * 0x1p-80f;
       store(vals ? sm.v[slot] : sm.k[slot], cw * 16, vals && zero);
       fence_proxy_async_smem();
       __syncwarp();
@@ -768,7 +768,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         if (!vals) {  // (the softmax is never a ring of these behind)
           const int at = here.step % kMetaSlots;
           sm.meta[at].ks[cw] = ks;
-          sm.meta[at].lvs[cw] = ph < 0 ? -INFINITY : zero ? kLvsFloor : lvs;
+          if (cw == 0) sm.meta[at].vref = here.vref;
+          sm.meta[at].lvs[cw] = ph < 0 ? -INFINITY : zero ? kLvsFloor : log2f(vs / here.vref);
           sm.meta[at].ivs[cw] = ph < 0 ? 0.f : zero ? 0x1p80f : here.vref / vs;
           mbar_arrive(&sm.meta_full[at]);
         }
