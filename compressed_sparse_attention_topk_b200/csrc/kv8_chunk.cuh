@@ -24,7 +24,7 @@
 //
 // Bound: 128 x 128 weights take 1,024 clocks of the exponential unit and
 // their two products the same of the tensor core.  2,048 tokens of 16 heads
-// over 16,384 positions (4 kv heads, D = 128) take 336 us, 767 TFLOP/s: some
+// over 16,384 positions (4 kv heads, D = 128) take 345 us, 747 TFLOP/s: some
 // 2,600 clocks for a step of both row tiles, which is the chain of one tile's
 // step (logits, maximum, weights, product) rather than any unit.
 #pragma once
