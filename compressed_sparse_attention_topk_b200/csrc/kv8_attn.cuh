@@ -239,11 +239,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
           (int64_t)p.s.lens[i] > ((int64_t)p.s.width << p.c.bs_shift))
         raise_status(kStatusBadIndex);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mine += __shfl_xor_sync(0xffffffffu, mine, o);
-      count += __shfl_xor_sync(0xffffffffu, count, o);
-    }
+    mine = warp_sum64(mine);
+    count = warp_sum64(count);
     if (lane == 0) {
       s_sum[warp] = mine;
       s_tiles[warp] = count;

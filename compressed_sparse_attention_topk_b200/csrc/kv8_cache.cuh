@@ -49,6 +49,12 @@ __device__ __forceinline__ long long warp_incl_scan64(long long v) {
   return v;
 }
 
+__device__ __forceinline__ long long warp_sum64(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 __device__ __forceinline__ int32_t sat32(long long v) {
   return v > 0x7fffffffll ? 0x7fffffff : (int32_t)v;
 }

@@ -30,6 +30,7 @@
 #pragma once
 
 #include "kv8_attn.cuh"
+#include "kv8_steps.cuh"
 #include "tcgen05.cuh"
 
 namespace csa2 {
@@ -37,10 +38,8 @@ namespace kv8 {
 
 using namespace tc;
 
-constexpr int kChunkKeys = 64;
 constexpr int kChunkGroups = kChunkKeys / 16;  // no page ends inside 16 positions
 constexpr int kChunkSlots = 4;                 // steps of fp16 tiles
-constexpr int kChunkRows = 256;
 constexpr int kSoftWarps = 8;
 constexpr int kConvWarps = 6;
 constexpr int kMmaWarps = 2;   // one per row tile; 16 warps in all: 128 registers a thread
@@ -245,12 +244,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 
 // ---------------------------------------------------------------------------
 // The line of steps (a tile's 64-key steps), cut evenly over the CTAs as in
-// kv8_attn.cuh.  A tile's steps end at its last row's position.
+// kv8_attn.cuh (kv8_steps.cuh counts them).
 // ---------------------------------------------------------------------------
-struct ChunkSeq {
-  int t0, T, pos0, tiles, reach;  // reach: positions that the table holds
-};
-
 __device__ __forceinline__ ChunkSeq chunk_seq(const AttnParams &p, int b) {
   ChunkSeq s;
   const int32_t lo = max(p.s.cu[b], 0), hi = p.s.cu[b + 1];
@@ -261,12 +256,6 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const AttnParams &p, int b) {
   s.tiles = rows <= p.split_rows ? 0 : (int)((rows + kChunkRows - 1) / kChunkRows);
   s.reach = p.s.width << p.c.bs_shift;
   return s;
-}
-
-__device__ __forceinline__ int chunk_steps(const ChunkSeq &s, int G, int x) {
-  const int rows = min((x + 1) * kChunkRows, s.T * G);
-  const int last = min(s.pos0 + (rows - 1) / G, s.reach - 1);
-  return last < 0 ? 1 : last / kChunkKeys + 1;
 }
 
 struct ChunkWalk {
@@ -374,9 +363,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   long long tiles = 0;
   for (int b = warp; b < p.s.B; b += kWarps) {
     const ChunkSeq s = chunk_seq(p, b);
-    int steps = 0;
-    for (int x = lane; x < s.tiles; x += 32) steps += chunk_steps(s, p.G, x);
-    steps = __reduce_add_sync(0xffffffffu, steps);
+    const long long steps = warp_sum64(chunk_steps_of(s, p.G, lane, 32));
     if (lane == 0) {
       per_seq[b] = steps;
       if (s.tiles > 0 && blockIdx.x == 0 && p.s.lens[b] > s.reach) raise_status(kStatusBadIndex);
@@ -387,8 +374,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
   __syncthreads();
   long long mine = 0;
   for (int b = tid; b < p.s.B; b += kChunkThreads) mine += per_seq[b];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  mine = warp_sum64(mine);
   if (lane == 0) sm.sum[warp] = mine;
   __syncthreads();
   long long W = 0;
@@ -432,7 +418,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     const ChunkSeq s = chunk_seq(p, b);
     const long long per = max(per_seq[b], 1ll);
     const int h = (int)((u0 - sm.pre) / per);
-    int r = (int)(u0 - sm.pre - h * per);  // steps of that head before u0
+    long long r = u0 - sm.pre - h * per;  // steps of that head before u0
     for (int x0 = 0; x0 < s.tiles; x0 += 32) {
       const int x = x0 + lane, n = x < s.tiles ? chunk_steps(s, p.G, x) : 0;
       const int incl = (int)warp_incl_scan((uint32_t)n);
@@ -441,7 +427,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         if (lane == __ffs(who) - 1) {
           sm.h = h;
           sm.x = x;
-          sm.from = r - (incl - n);
+          sm.from = (int)r - (incl - n);
         }
         break;
       }
