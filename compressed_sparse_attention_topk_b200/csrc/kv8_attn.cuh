@@ -19,6 +19,7 @@
 #include <cuda.h>
 
 #include "kv8_cache.cuh"
+#include "kv8_steps.cuh"
 
 namespace csa2 {
 namespace kv8 {
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
     pre = s_pre;
   }
 
-  int n_issued = 0;     // units issued by this warp so far: stage and phase
+  int n_issued = 0;     // units issued by this warp so far, in two rounds of the ring
   bool broken = false;  // a copy did not arrive: this warp reads no more
   int4 rec = make_int4(-1, 0, 0, 0);
   for (long long u = u0; u < u1;) {
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
       __syncwarp();
       if (i + kStages < mine) issue(i + kStages);
     }
-    n_issued = base + mine;
+    n_issued = ring_after(base, mine, kStages);
 
     // ---- the warps' results into their rings, then merged ----
     float *res = reinterpret_cast<float *>(ring);

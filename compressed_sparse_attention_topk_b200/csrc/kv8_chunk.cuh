@@ -30,7 +30,6 @@
 #pragma once
 
 #include "kv8_attn.cuh"
-#include "kv8_steps.cuh"
 #include "tcgen05.cuh"
 
 namespace csa2 {
@@ -454,12 +453,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     const uint32_t lane_at = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_o = tmem + lane_at + 256u + (uint32_t)(tile * D);
     uint32_t n_steps = 0;    // of this tile so far: buffers and phases
-    int k_index = 0;         // steps of both tiles so far: slots of the page facts
+    uint32_t k_index = 0;    // steps of both tiles so far: slots of the page facts
     int4 rec = make_int4(-1, 0, 0, 0);
     do {
       const bool whole = walk.first == 0 && walk.last == walk.steps;
       if (tile * 128 >= walk.nrows) {  // warp-uniform: no row of this tile
-        k_index += walk.last - walk.first;
+        k_index += (uint32_t)(walk.last - walk.first);
         continue;
       }
       const int r = tile * 128 + row;
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
 
       float m = -INFINITY, l = 0.f;
       for (int t = walk.first; t < walk.last; ++t, ++k_index, ++n_steps) {
-        const ChunkMeta &me = sm.meta[k_index % kMetaSlots];
+        const ChunkMeta &me = sm.meta[ring_slot<kMetaSlots>(k_index)];
         // the products first: once they are there, the page facts of this very
         // step are (a row tile that skipped steps could mistake an older phase)
         const uint32_t buf = n_steps & 1u, phase = (n_steps >> 1) & 1u;
@@ -517,8 +516,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
         uint32_t a[32], b2[32];
         tmem_ld32(t_s, a);
         tmem_ld32(t_s + 32, b2);
-        ok = chunk_wait(sm, &sm.meta_full[k_index % kMetaSlots],
-                        (uint32_t)(k_index / kMetaSlots) & 1u);
+        ok = chunk_wait(sm, &sm.meta_full[ring_slot<kMetaSlots>(k_index)],
+                        ring_parity<kMetaSlots>(k_index));
         const int seen = my_pos - t * kChunkKeys;  // columns 0 .. seen are visible
         float fk[4], lv[4];
 #pragma unroll
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const float zero = m - kPBias;
       float *part = p.part + (2 * c + (walk.first > 0 ? 0 : 1)) * S::PART;
       // (a partial is kept in units 2^24 larger: O vref stays in range)
-      const float vref = sm.meta[(k_index - 1) % kMetaSlots].vref;  // (not written again yet)
+      const float vref = sm.meta[ring_slot<kMetaSlots>(k_index - 1)].vref;  // (not yet rewritten)
       const float mul = whole ? (l == 0.f ? 0.f : vref / l) : vref * 0x1p-24f;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -662,14 +661,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     // Where a step's positions are: their page as the table has it (on the way
     // from one iteration to the next), and what it takes to use it.
     struct Place {
-      int step, part;      // part: 0 .. 3 keys, 4 .. 7 values
+      uint32_t step;       // of the CTA
+      int part;            // 0 .. 3 keys, 4 .. 7 values
       int raw, key, h;     // table entry, first position, kv head
       bool seen;           // the entry was read: the positions are seen
       float vref;
     };
     int t = walk.first;
     float vref_now = chunk_vref(p, walk.b, walk.h);
-    int step = 0, part = warp - kSoftWarps;  // of the task that `look` is at
+    uint32_t step = 0;  // of the task that `look` is at
+    int part = warp - kSoftWarps;
     auto look = [&](Place &at) {
       at.step = step;
       at.part = part;
@@ -737,12 +738,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     float ks = ph >= 0 ? p.c.k_scale[ph] : 0.f, vs = ph >= 0 ? p.c.v_scale[ph] : 0.f;
     load(ph, here);
     for (;;) {
-      const int slot = here.step % kChunkSlots;
+      const int slot = ring_slot<kChunkSlots>(here.step);
       const int cw = here.part % kChunkGroups;
       const bool vals = here.part >= kChunkGroups;
-      if (here.step >= kChunkSlots &&
-          !chunk_wait(sm, vals ? &sm.v_empty[slot] : &sm.k_empty[slot],
-                      (uint32_t)(here.step / kChunkSlots - 1) & 1u))
+      if (!chunk_wait(sm, vals ? &sm.v_empty[slot] : &sm.k_empty[slot],
+                      ring_parity<kChunkSlots>(here.step) ^ 1u))
         break;
       // (a page without values must not raise the maximum: it takes the floor)
       const bool zero = vs == 0.f || vs < here.vref * 0x1p-80f;
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       if (lane == 0) {
         mbar_arrive(vals ? &sm.v_full[slot] : &sm.k_full[slot]);
         if (!vals) {  // (the softmax is never a ring of these behind)
-          const int at = here.step % kMetaSlots;
+          const int at = ring_slot<kMetaSlots>(here.step);
           sm.meta[at].ks[cw] = ks;
           if (cw == 0) sm.meta[at].vref = here.vref;
           sm.meta[at].lvs[cw] = ph < 0 ? -INFINITY : zero ? kLvsFloor : log2f(vs / here.vref);
@@ -776,15 +776,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
     const int tile = warp - kSoftWarps - kConvWarps;
     constexpr uint32_t kIdQK = chunk_idesc(kChunkKeys, false), kIdPV = chunk_idesc(D, true);
     uint32_t n_seg = 0u, n_s = 0u, n_p = 0u;  // tiles, logits and weights so far
-    int k_index = 0;
+    uint32_t k_index = 0u;
     bool ok = true;
     const uint64_t q_desc = chunk_desc(sm.q[tile], 16), k_desc = chunk_desc(sm.k[0], 16);
     const uint64_t v_desc = chunk_desc(sm.v[0], S::SUB);
     const uint32_t t_s = tmem + (uint32_t)(tile * 128), t_o = tmem + 256u + (uint32_t)(tile * D);
     // the logits of step k
-    auto qk = [&](int k) {
-      const int slot = k % kChunkSlots;
-      ok = chunk_wait(sm, &sm.k_full[slot], (uint32_t)(k / kChunkSlots) & 1u);
+    auto qk = [&](uint32_t k) {
+      const int slot = ring_slot<kChunkSlots>(k);
+      ok = chunk_wait(sm, &sm.k_full[slot], ring_parity<kChunkSlots>(k));
       if (!ok) return;
       tc_fence_after();
       const uint32_t buf = n_s++ & 1u;
@@ -800,8 +800,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       const int n = walk.last - walk.first;
       if (tile * 128 >= walk.nrows) {  // no row of this tile: the slots pass by
         for (int t = 0; t < n && ok; ++t, ++k_index) {
-          const int slot = k_index % kChunkSlots;
-          const uint32_t phase = (uint32_t)(k_index / kChunkSlots) & 1u;
+          const int slot = ring_slot<kChunkSlots>(k_index);
+          const uint32_t phase = ring_parity<kChunkSlots>(k_index);
           ok = chunk_wait(sm, &sm.k_full[slot], phase);
           if (ok) mbar_arrive(&sm.k_empty[slot]);
           ok = ok && chunk_wait(sm, &sm.v_full[slot], phase);
@@ -814,10 +814,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv8_chunk_kernel(const AttnP
       // soon as the product of its weights has been issued
       for (int at = 0; at < min(n, 2) && ok; ++at) qk(k_index + at);
       for (int t = 0; t < n && ok; ++t, ++k_index) {
-        const int slot = k_index % kChunkSlots;
+        const int slot = ring_slot<kChunkSlots>(k_index);
         const uint32_t buf = n_p & 1u, phase = (n_p >> 1) & 1u;
         ++n_p;
-        ok = chunk_wait(sm, &sm.v_full[slot], (uint32_t)(k_index / kChunkSlots) & 1u) &&
+        ok = chunk_wait(sm, &sm.v_full[slot], ring_parity<kChunkSlots>(k_index)) &&
              chunk_wait(sm, &sm.p_full[tile][buf], phase);
         if (!ok) break;
         tc_fence_after();

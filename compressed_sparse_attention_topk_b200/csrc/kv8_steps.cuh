@@ -1,6 +1,6 @@
-// Steps of the many-row attention's line of work (kv8_chunk.cuh).  Host code
-// too, so that the counts can be checked as whole numbers at sizes that no
-// test attends over.
+// Counts of the attention kernels' work: steps of the many-row attention's
+// line (kv8_chunk.cuh), uses of a ring of buffers.  Host code too, so that
+// they can be checked as whole numbers at sizes that no test attends over.
 #pragma once
 
 #include <cstdint>
@@ -32,6 +32,27 @@ __host__ __device__ inline long long chunk_steps_of(const ChunkSeq &s, int G, in
   long long steps = 0;
   for (int x = x0; x < s.tiles; x += stride) steps += chunk_steps(s, G, x);
   return steps;
+}
+
+// The n-th use of a ring of SLOTS buffers: which one, and the parity of the
+// barrier phase that this use completes.  A block may use a ring more than
+// 2^32 times: the count then wraps, which a power of two of slots does not
+// notice.  (Waiting for the phase before the first, parity 1 of a barrier just
+// made, is answered at once.)
+template <int SLOTS>
+__host__ __device__ inline int ring_slot(uint32_t n) {
+  static_assert((SLOTS & (SLOTS - 1)) == 0, "a wrapped count must stay in step");
+  return (int)(n % SLOTS);
+}
+template <int SLOTS>
+__host__ __device__ inline uint32_t ring_parity(uint32_t n) {
+  return (n / SLOTS) & 1u;
+}
+
+// A ring of any number of slots: the count after `used` (at most 2^26) more
+// uses, kept below two rounds, which leaves slot and parity as they are.
+__host__ __device__ inline int ring_after(int n, int used, int slots) {
+  return (n + used) % (2 * slots);
 }
 
 }  // namespace kv8

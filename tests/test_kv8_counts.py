@@ -13,8 +13,29 @@ PROGRAM = r"""
 #include "kv8_steps.cuh"
 using namespace csa2::kv8;
 
-// steps T pos0 G reach: the sum over a warp's lanes, then the last tile's
+template <int SLOTS>
+int ring(long long n) {  // use n of a ring against its 64-bit count
+  return ring_slot<SLOTS>((uint32_t)n) == n % SLOTS &&
+         ring_parity<SLOTS>((uint32_t)n) == (uint32_t)(n / SLOTS & 1);
+}
+
 int main(int argc, char **argv) {
+  if (argc == 2) {  // uses of a ring of any size, in tiles of so many
+    const int used = atoi(argv[1]);
+    long long n = 0;
+    for (int slots = 2; slots <= 6; ++slots) {
+      int base = 0;
+      for (n = 0; n < (5ll << 31); n += used, base = ring_after(base, used, slots))
+        if (base < 0 || base >= 2 * slots || base % slots != n % slots ||
+            (base / slots & 1) != (n / slots & 1))
+          return 1;
+    }
+    for (n = -3; n <= 3; ++n)
+      for (long long at : {4ll, 1ll << 31, 1ll << 32, 3ll << 32})
+        if (!ring<4>(at + n) || !ring<8>(at + n)) return 1;
+    return 0;
+  }
+  // T pos0 G reach: a sequence's steps (the sum over a warp's lanes), the last tile's
   const long long T = atoll(argv[1]), pos0 = atoll(argv[2]), G = atoll(argv[3]);
   ChunkSeq s{};
   s.T = (int)T;
@@ -70,3 +91,9 @@ def test_rows_that_end_at_the_limit_of_32_bits(program):
     assert last == (T - 1) // 64 + 1
     # two tokens to a tile, 32 tiles to a step count (the last tile: one token)
     assert total == sum(32 * k for k in range(1, last + 1))
+
+
+@pytest.mark.parametrize("used", [1 << 25, (1 << 25) - 1, 1000003])
+def test_rings_used_more_than_2_to_the_32_times(program, used):
+    """Slot and phase of every use follow the 64-bit count."""
+    assert program(used) == []
