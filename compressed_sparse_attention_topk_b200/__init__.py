@@ -710,8 +710,8 @@ def kv8_attn(q, cache: KV8Cache, table, cu, lens, sel=None, sm_scale: Optional[f
              out=None, lse=None, ws=None):
     """Causal attention of a step's tokens over the cache (their own keys and
     values already appended): q bf16 [n, H, D], table int32 [B, width], cu
-    int32 [B+1], lens int32 [B]; sel int32 [n, Hk, n_sel]: only the listed
-    blocks -> (out bf16 [n, H, D], lse fp32 [n, H])."""
+    int32 [B+1], lens int32 [B]; sel int32 [n, Hk, n_sel >= 1]: only the
+    listed blocks -> (out bf16 [n, H, D], lse fp32 [n, H])."""
     torch, i32, _, bf16, f32, _ = _kv8_types()
     dev = torch.cuda.current_device()
     D = cache.D
@@ -721,6 +721,8 @@ def kv8_attn(q, cache: KV8Cache, table, cu, lens, sel=None, sm_scale: Optional[f
     if sel is not None:
         if _check_dense(sel, "sel", i32, dev).dim() != 3 or sel.shape[:2] != (n, cache.Hk):
             raise ValueError("sel must be [n, Hk, n_sel]")
+        if sel.shape[2] == 0:  # (the C call takes a null pointer as every block)
+            raise ValueError("sel must have room for a block: n_sel >= 1")
         sel_ptr, n_sel = sel.data_ptr(), sel.shape[2]
     if out is None:
         out = q.new_empty((n, H, D))

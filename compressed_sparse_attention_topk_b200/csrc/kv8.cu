@@ -422,9 +422,9 @@ csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *c
   kv8::AttnParams p{};
   csa2_status rc = cache_view(cache, &p.c);
   if (rc != CSA2_OK) return rc;
-  if (n < 0 || B < 0 || n_sel < 0 || (sel != nullptr) != (n_sel > 0) || !std::isfinite(sm_scale))
-    return CSA2_ERR_INVALID_ARG;
+  if (n < 0 || B < 0 || n_sel < 0 || !std::isfinite(sm_scale)) return CSA2_ERR_INVALID_ARG;
   if (n == 0 || B == 0) return CSA2_OK;
+  if ((sel != nullptr) != (n_sel > 0)) return CSA2_ERR_INVALID_ARG;
   rc = check_step(q, q_stride, p.c, table, width, cu, lens, B, H);
   if (rc != CSA2_OK) return rc;
   if (!out || !aligned(out, 16) || !aligned(lse, 4) || !aligned(sel, 4))

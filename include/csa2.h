@@ -558,8 +558,9 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
  * A sequence with more new tokens than lens has tokens at negative positions,
  * which see nothing.
  *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
- *   sel  device, int32 [n, Hk, n_sel] or NULL (n_sel 0): block numbers of the
- *        sequence, each at most once, a negative one is skipped
+ *   sel  device, int32 [n, Hk, n_sel] with n_sel >= 1, or NULL and n_sel 0
+ *        (every block): block numbers of the sequence, each at most once, a
+ *        negative one is skipped
  *   out  device, bf16 [n, H, D] (16-byte aligned); lse device, fp32 [n, H] or
  *        NULL
  *   ws   device workspace of ws_bytes >= csa2_kv8_attn_workspace_size

@@ -1,0 +1,57 @@
+"""Calls at the edge of what the 8-bit paged cache's documentation allows, on
+the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import compressed_sparse_attention_topk_b200 as csa2
+from compressed_sparse_attention_topk_b200 import build as csa2_build
+from tests import _kv8 as ref
+from tests.test_gpu_kv8 import check_attn, dev, dev_bf16, gpu_cache, make_step
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    csa2_build.build()
+    csa2.lib()
+    csa2.get_device_status()
+
+
+def small_step(rng, lens, adds, H, Hk, D, bs, **kw):
+    """(q, cache, table, cu, lens) of a step as host arrays and as the calls
+    take them."""
+    table, cu, P = make_step(rng, lens, adds, bs, **kw)
+    c = ref.new_cache(rng, P, Hk, bs, D)
+    q = ref.bf16(rng.standard_normal((int(cu[-1]), H, D)).astype(np.float32))
+    host = (q, c, table, cu, np.array(lens, np.int32))
+    return host, (dev_bf16(q), gpu_cache(c), dev(table), dev(cu), dev(host[4]))
+
+
+def test_lists_without_a_place_are_refused():
+    """They must not mean every block, which a list tensor's null pointer does."""
+    _, args = small_step(np.random.default_rng(1), [70, 9], [2, 1], 4, 2, 64, 32)
+    sel = torch.empty((3, 2, 0), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        csa2.kv8_attn(*args, sel=sel)
+    out, lse = csa2.kv8_attn(*args, sel=torch.full((3, 2, 1), -1, dtype=torch.int32,
+                                                   device="cuda"))
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert csa2.get_device_status() == 0
+
+
+def test_a_step_without_tokens():
+    _, (q, c, table, cu, lens) = small_step(np.random.default_rng(2), [70, 9], [1, 0], 4, 2, 64,
+                                            32)
+    q, cu = q[:0], torch.zeros_like(cu)
+    sel = csa2.kv8_select(q, c, table, cu, lens, 3)
+    assert sel.shape == (0, 2, 3)
+    for s in (None, sel):
+        out, lse = csa2.kv8_attn(q, c, table, cu, lens, sel=s)
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    none = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(0, dtype=torch.int64, device="cuda")
+    csa2.kv8_append(c, none, none, slots)
+    assert csa2.kv8_unpack(c, slots)[0].shape == (0, 2, 64)
+    assert csa2.get_device_status() == 0
