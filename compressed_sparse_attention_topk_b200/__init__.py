@@ -524,11 +524,11 @@ def _check_tokens(t, name, D, heads, dev):
     s0, s1, s2 = t.stride()
     if d != D or (heads is not None and h != heads):
         raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {D}]")
-    if s2 != 1 or (h > 1 and s1 != D):
+    if n > 0 and (s2 != 1 or (h > 1 and s1 != D)):
         raise ValueError(f"{name}: the heads of a token must be dense")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return n, h, (s0 if n > 1 else max(s0, h * D))
+    return n, h, (s0 if n > 1 else h * D)  # (one token's stride leads nowhere)
 
 
 def _check_step(cache, table, cu, lens, dev):

@@ -55,3 +55,27 @@ def test_a_step_without_tokens():
     csa2.kv8_append(c, none, none, slots)
     assert csa2.kv8_unpack(c, slots)[0].shape == (0, 2, 64)
     assert csa2.get_device_status() == 0
+
+
+def test_strides_that_address_nothing_are_not_looked_at():
+    """One token of a projection of odd width, no token with strides of its
+    own: the same results as from dense tensors."""
+    (q, c, table, cu, lens), args = small_step(np.random.default_rng(3), [150], [1], 4, 2, 64, 32)
+    want = csa2.kv8_attn(*args)
+    wide = torch.zeros((1, 4 * 64 + 2 * 2 * 64 + 1), dtype=torch.bfloat16, device="cuda")
+    wide[:, :256] = args[0].view(1, 256)
+    one = wide.as_strided((1, 4, 64), (wide.shape[1], 64, 1))
+    assert one.stride(0) % 8 != 0
+    got = csa2.kv8_attn(one, *args[1:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    sel = csa2.kv8_select(one, *args[1:], 3)
+    assert torch.equal(sel, csa2.kv8_select(*args, 3))
+    new = wide[:, 256:].as_strided((1, 2, 64), (wide.shape[1], 64, 1))
+    csa2.kv8_append(args[1], new, new, dev(np.array([3], np.int64)))
+    none = torch.empty_strided((0, 4, 64), (1, 1, 1), dtype=torch.bfloat16, device="cuda")
+    assert csa2.kv8_attn(none, *args[1:])[0].shape == (0, 4, 64)
+    assert csa2.kv8_select(none, *args[1:], 3).shape == (0, 2, 3)
+    two = torch.zeros((2, 4 * 64 + 1), dtype=torch.bfloat16, device="cuda")[:, :256].view(2, 4, 64)
+    with pytest.raises(csa2.CSA2Error):
+        csa2.kv8_attn(two, *args[1:])
+    assert csa2.get_device_status() == 0
