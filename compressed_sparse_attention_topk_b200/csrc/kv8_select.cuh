@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) kv8_score_kernel(const Selec
   const int64_t tok0 = cu0 + x0;
   const int64_t pos_last = (int64_t)p.s.lens[b] - cu1 + tok0 + count - 1;
   const int nblk = seen_blocks(pos_last, p.c.bs_shift, p.s.width);
+  if (tid == 0 && blockIdx.y == 0 && blockIdx.z == 0 && pos_last >> p.c.bs_shift >= p.s.width)
+    raise_status(kStatusBadIndex);  // (blocks past the table's width)
   const int groups = (nblk + 15) / 16;
   const int stride = kScoreWarps * gridDim.z;
   int gi = blockIdx.z * kScoreWarps + warp;

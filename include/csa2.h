@@ -532,7 +532,9 @@ size_t csa2_kv8_select_workspace_size(int64_t n, int32_t Hk, int32_t width);
  *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
  *   sel  device, int32 [n, Hk, n_sel] (output): blocks ascending, then -1
  *   ws   device workspace of ws_bytes >= csa2_kv8_select_workspace_size
- * A block whose page is outside the cache scores lowest of all.
+ * A block whose page is outside the cache scores lowest of all.  Blocks past
+ * the table's width are not there (recorded, bit 0): the last n_last are then
+ * the table's last ones, not the token's own.
  * Supported: H a multiple of Hk, H <= 128, 1 <= n_sel <= 4096, n_first >= 0,
  * n_last >= 1 (the block being filled is always kept), n_first + n_last <=
  * n_sel, width <= 65536, B <= 4096, n * Hk < 2^31. */

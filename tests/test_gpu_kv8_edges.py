@@ -79,3 +79,39 @@ def test_strides_that_address_nothing_are_not_looked_at():
     with pytest.raises(csa2.CSA2Error):
         csa2.kv8_attn(two, *args[1:])
     assert csa2.get_device_status() == 0
+
+
+# --- choice of blocks ---------------------------------------------------------
+
+def check_select(host, args, n_sel, n_first=1, n_last=1):
+    q, c, table, cu, lens = host
+    want = np.full((len(q), c["k"].shape[1], n_sel), -7, np.int32)
+    ref.select(q, c, table, cu, lens, n_sel, n_first, n_last, want)
+    got = torch.full(want.shape, -7, dtype=torch.int32, device="cuda")
+    csa2.kv8_select(*args, n_sel, n_first, n_last, out=got)
+    got = got.cpu().numpy()
+    assert np.array_equal(got, want), np.argwhere((got != want).any(-1))[:5]
+
+
+@pytest.mark.parametrize("lens,adds,width", [([500], [1], 9), ([40, 700, 16], [2, 300, 1], 12),
+                                             ([289], [1], 9)])
+def test_select_records_a_table_narrower_than_the_sequence(lens, adds, width):
+    """Blocks past the table's width do not exist; that is recorded."""
+    (q, c, table, cu, lens), args = small_step(np.random.default_rng(4), lens, adds, 4, 2, 64, 32)
+    table = np.ascontiguousarray(table[:, :width])
+    check_select((q, c, table, cu, lens), (*args[:2], dev(table), *args[3:]), 5)
+    assert csa2.get_device_status() == 1
+    # of the same width, no longer than the table: nothing to record
+    lens = np.minimum(lens, width * 32)
+    check_select((q, c, table, cu, lens), (*args[:2], dev(table), *args[3:4], dev(lens)), 5)
+    assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,adds,extra_width", [([900, 20], [3, 1], 41000),
+                                                   ([41500 * 16 - 3], [2], 3)])
+def test_select_of_rows_wider_than_shared_memory(lens, adds, extra_width):
+    host, args = small_step(np.random.default_rng(5), lens, adds, 2, 1, 64, 16,
+                            extra_width=extra_width)
+    assert host[2].shape[1] > 40960
+    check_select(host, args, 40, 2, 3)
+    assert csa2.get_device_status() == 0
