@@ -268,7 +268,10 @@ __global__ void __launch_bounds__(32 * kPickWarps) kv8_pick_warp_kernel(const Se
   const int64_t i = item / p.c.Hk;
   if (i >= p.s.n) return;
   const int b = seq_of(p.s, i, lane);
-  if (b < 0) return;
+  if (b < 0) {
+    pdl_wait_primary();  // (or this launch, and what follows it, could overtake the scores')
+    return;
+  }
   const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
   const int nblk = seen_blocks(pos, p.c.bs_shift, p.s.width);
   int32_t *out = p.sel + item * p.n_sel;
@@ -353,7 +356,10 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_cta_kernel(const Select
   const int64_t item = blockIdx.x;
   const int64_t i = item / p.c.Hk;
   const int b = seq_of(p.s, i, lane);
-  if (b < 0) return;
+  if (b < 0) {
+    pdl_wait_primary();  // (as above)
+    return;
+  }
   const int64_t pos = (int64_t)p.s.lens[b] - p.s.cu[b + 1] + i;
   const int nblk = seen_blocks(pos, p.c.bs_shift, p.s.width);
   for (int k = tid; k < kBins1; k += kPickThreads) s_hist[k] = 0u;

@@ -115,3 +115,19 @@ def test_select_of_rows_wider_than_shared_memory(lens, adds, extra_width):
     assert host[2].shape[1] > 40960
     check_select(host, args, 40, 2, 3)
     assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("extra_width", [1, 3000])
+def test_select_of_padding_alone_with_calls_behind_it(extra_width):
+    """Steps whose tokens all belong to nobody write nothing, and the calls
+    behind them find their inputs as they left them."""
+    host, args = small_step(np.random.default_rng(6), [900, 20], [3, 1], 4, 2, 64, 16,
+                            extra_width=extra_width)
+    none = torch.zeros_like(args[3])
+    for _ in range(20):
+        out = torch.full((4, 2, 8), -7, dtype=torch.int32, device="cuda")
+        csa2.kv8_select(*args[:3], none, args[4], 8, out=out)
+        args[3].copy_(args[3].clone())
+        check_select(host, args, 8)
+        assert (out == -7).all()
+    assert csa2.get_device_status() == 0
