@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
       tl.pos0 = pos0;
       tl.units = units;
     }
-    tl.pos_first = tl.pos0 + tl.row0 / p.G;
+    // (at most as a row's own position below: a missing page's, kNoPos, is past it)
+    tl.pos_first = min(tl.pos0 + tl.row0 / p.G, kNoPos - 1);
     tl.pos_last = tl.pos0 + (tl.row0 + tl.nrows - 1) / p.G;
     const int first = (int)(u - tile_begin);
     const int last = (int)min(u1 - tile_begin, (long long)tl.units);  // units [first, last)

@@ -131,3 +131,28 @@ def test_select_of_padding_alone_with_calls_behind_it(extra_width):
         check_select(host, args, 8)
         assert (out == -7).all()
     assert csa2.get_device_status() == 0
+
+
+# --- attention ----------------------------------------------------------------
+
+@pytest.mark.parametrize("H,D,T", [(4, 64, 1), (8, 128, 1), (16, 128, 2)])
+def test_attn_a_missing_page_of_16_under_a_position_past_2_to_the_30(H, D, T):
+    """Lengths past every table's reach: the missing half of a unit of two
+    pages (a bad page, or the end of a list) is not seen."""
+    rng = np.random.default_rng(7)
+    (q, c, table, cu, _), args = small_step(rng, [16], [T], H, 2, D, 16)
+    table = np.array([[table[0, 0], -1]], np.int32)
+    lens = dev(np.array([(1 << 30) + 100], np.int32))
+    # every token sees the page whole, as a single one at its last position does
+    want = [np.zeros((T, H, D)), np.zeros((T, H))]
+    info = [np.zeros((T, H, D))] + [np.zeros((T, H)) for _ in range(3)]
+    for i in range(T):
+        out, lse, more = ref.attn(q[i:i + 1], c, table, np.array([0, 1]), [16])
+        for x, y in zip(want + info, (out, lse) + more):
+            x[i] = y[0]
+    args = (*args[:2], dev(table), args[3], lens)
+    check_attn(*csa2.kv8_attn(*args), *want, info, T)
+    assert csa2.get_device_status() == 1
+    sel = torch.zeros((T, 2, 1), dtype=torch.int32, device="cuda")
+    check_attn(*csa2.kv8_attn(*args, sel=sel), *want, info, T)
+    assert csa2.get_device_status() == 0
