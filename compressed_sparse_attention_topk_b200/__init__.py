@@ -567,7 +567,8 @@ def block_tables(lens, add, table, free_pages, block: int, cap: int, out=None):
     (int32 [B, width], updated).  Returns (lens + add int32 [B], cu int32
     [B+1], slots int64 [cap], pos int32 [cap], used int32 [1]): token offsets,
     each token's slot (page * block + row) and position (-1 past the last
-    token), pages taken.  ``out``: those five tensors, to write into."""
+    token), pages taken.  ``out``: those five tensors, to write into (they
+    overlap nothing else)."""
     torch, i32, i64 = _kv8_types()[:3]
     dev = torch.cuda.current_device()
     _check_dense(lens, "lens", i32, dev)

@@ -66,6 +66,23 @@ csa2_status check_step(const uint16_t *q, int64_t q_stride, const kv8::Cache &c,
   return CSA2_OK;
 }
 
+struct Bytes {
+  const void *at;
+  size_t n;
+};
+
+// Whether any of the first `written` ranges shares a byte with another range.
+template <size_t N>
+bool overlap(const Bytes (&r)[N], size_t written) {
+  for (size_t i = 0; i < written; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].at);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(r[j].at);
+      if (r[i].n && r[j].n && a < b + r[j].n && b < a + r[i].n) return true;
+    }
+  return false;
+}
+
 template <int D, int BS>
 void launch_append(const kv8::AppendParams &p, cudaStream_t st) {
   const dim3 grid((unsigned)ceil_div(p.n, p.group), (unsigned)p.c.Hk, 2);
@@ -300,7 +317,6 @@ csa2_status csa2_block_tables(const int32_t *lens, const int32_t *add, int32_t B
   if (B < 0 || width < 1 || n_free < 0 || cap < 0 || block < 1) return CSA2_ERR_INVALID_ARG;
   if (!cu || !used || (B > 0 && (!lens || !add || !table || !lens_out)) ||
       (n_free > 0 && !free_pages) || (cap > 0 && (!slots || !pos)) ||
-      (B > 0 && (lens_out == lens || lens_out == add)) ||
       !aligned(lens, 4) || !aligned(add, 4) || !aligned(table, 4) || !aligned(free_pages, 4) ||
       !aligned(lens_out, 4) || !aligned(cu, 4) || !aligned(used, 4) || !aligned(slots, 8) ||
       !aligned(pos, 4))
@@ -309,6 +325,14 @@ csa2_status csa2_block_tables(const int32_t *lens, const int32_t *add, int32_t B
   if (shift < 0 || B > kv8::kMaxSeqs || int64_t(width) * block >= (int64_t(1) << 31) ||
       cap >= (int64_t(1) << 31))
     return CSA2_ERR_UNSUPPORTED;
+  // every block reads the lengths, the lists and the tables again
+  const size_t b4 = size_t(B) * 4;
+  const Bytes ranges[] = {{lens_out, b4},           {cu, b4 + 4},
+                          {slots, size_t(cap) * 8}, {pos, size_t(cap) * 4},
+                          {used, 4},                {table, b4 * width},
+                          {lens, b4},               {add, b4},
+                          {free_pages, size_t(n_free) * 4}};
+  if (overlap(ranges, 6)) return CSA2_ERR_INVALID_ARG;
   const kv8::TableParams p{lens, add, table, free_pages, lens_out, cu,    slots, pos,
                            used, cap, B,     shift,      width,    n_free};
   const int64_t blocks = std::min<int64_t>(

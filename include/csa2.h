@@ -479,12 +479,14 @@ typedef struct csa2_kv8 {
  *               recorded in the device status word, bit 2)
  *   table       device, int32 [B, width]: the new pages' entries are written
  *   free_pages  device, int32 [n_free]
- *   lens_out    device, int32 [B]     lens + add (not lens or add itself)
+ *   lens_out    device, int32 [B]     lens + add
  *   cu          device, int32 [B+1]   token offsets of the requests
  *   slots       device, int64 [cap]   page * block + row of every token of the
  *               step, in request order; -1 from the last token on
  *   pos         device, int32 [cap]   its position; -1 from the last token on
  *   used        device, int32 [1]     pages taken from the free list
+ * What is written (table, lens_out, cu, slots, pos, used) overlaps nothing
+ * else: no update in place but the table's.
  * When the free list is too short, or a request outgrows its table row, the
  * tokens without a page get slot -1 and the entries without one -1; tokens
  * past cap are not written; each is recorded in the status word (bit 2), and

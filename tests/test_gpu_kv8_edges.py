@@ -81,6 +81,32 @@ def test_strides_that_address_nothing_are_not_looked_at():
     assert csa2.get_device_status() == 0
 
 
+# --- block tables -------------------------------------------------------------
+
+@pytest.mark.parametrize("B,cap", [(3, 9), (0, 2), (2, 0)])
+def test_block_tables_on_buffers_side_by_side(B, cap):
+    """Parts of one buffer, with nothing between them."""
+    rng = np.random.default_rng(8)
+    lens, add = rng.integers(0, 40, B).astype(np.int32), rng.integers(0, 3, B).astype(np.int32)
+    table = rng.integers(0, 50, (B, 4)).astype(np.int32)
+    free = np.arange(60, 70, dtype=np.int32)
+    want = ref.block_tables(lens, add, table, free, 16, cap)
+    buf = torch.zeros(2 * cap + cap + 8 * B + 12, dtype=torch.int32, device="cuda")
+    s, p, a, b, t, f, o, u, n = buf.split((2 * cap, cap, B, B, 4 * B, 10, B, B + 1, 1)
+                                          if B else (2 * cap, cap, 0, 0, 0, 10, 0, 1, 1))
+    for x, y in ((a, lens), (b, add), (t, table.reshape(-1)), (f, free)):
+        x.copy_(dev(y))
+    out = (o, u, s.view(torch.int64), p, n)
+    csa2.block_tables(a, b, t.view(B, 4), f, 16, cap, out=out)
+    for x, y in zip(out + (t,), want):
+        assert np.array_equal(x.cpu().numpy(), np.reshape(y, -1))
+    assert csa2.get_device_status() == (4 if cap < int(add.sum()) else 0)
+    if B:
+        with pytest.raises(csa2.CSA2Error):
+            csa2.block_tables(a, b, t.view(B, 4), f, 16, cap, out=(buf[3 * cap:3 * cap + B],
+                                                                   *out[1:]))
+
+
 # --- choice of blocks ---------------------------------------------------------
 
 def check_select(host, args, n_sel, n_first=1, n_last=1):
