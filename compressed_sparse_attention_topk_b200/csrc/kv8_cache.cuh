@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
         if (f < p.n_free) page = p.free_pages[f];
       }
       if (page >= 0) slot = ((int64_t)page << p.bs_shift) + (pos & bs1);
+      else bad = true;
       at = sat32(pos);
     }
     p.slots[i] = slot;

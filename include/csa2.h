@@ -488,7 +488,8 @@ typedef struct csa2_kv8 {
  * What is written (table, lens_out, cu, slots, pos, used) overlaps nothing
  * else: no update in place but the table's.
  * When the free list is too short, or a request outgrows its table row, the
- * tokens without a page get slot -1 and the entries without one -1; tokens
+ * tokens without a page get slot -1 and the entries without one -1 (and so do
+ * the tokens of a page that was missing before: a negative entry); tokens
  * past cap are not written; each is recorded in the status word (bit 2), and
  * `used` still counts what was asked for.
  * Supported: 0 <= B <= 4096, width * block < 2^31, cap < 2^31. */

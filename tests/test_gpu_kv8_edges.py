@@ -107,6 +107,27 @@ def test_block_tables_on_buffers_side_by_side(B, cap):
                                                                    *out[1:]))
 
 
+def test_block_tables_records_tokens_of_a_page_that_was_never_there():
+    """A request whose last page is missing (a free list too short the step
+    before): its tokens have no slot, and the status word says so each time."""
+    lens, add = np.array([20, 16, 5], np.int32), np.array([3, 2, 1], np.int32)
+    table = np.array([[7, -1, 9], [3, 4, 9], [6, 9, 9]], np.int32)
+    free = np.array([11, 12], np.int32)
+    for t, a, status in ((table, add, 4), (table, np.array([0, 2, 1], np.int32), 0),
+                         (np.abs(table), add, 0)):
+        want = ref.block_tables(lens, a, t, free, 16, 8)
+        g = dev(t)
+        got = csa2.block_tables(dev(lens), dev(a), g, dev(free), 16, 8)
+        for x, y in zip(got + (g,), want):
+            assert np.array_equal(x.cpu().numpy().reshape(-1), np.reshape(y, -1))
+        assert csa2.get_device_status() == status
+    # a page that the free list lends is none either
+    got = csa2.block_tables(dev(lens), dev(add), dev(np.abs(table)), dev(np.array([-5], np.int32)),
+                            16, 8)
+    assert (got[2][3:5] == -1).all() and got[4].item() == 1
+    assert csa2.get_device_status() == 4
+
+
 # --- choice of blocks ---------------------------------------------------------
 
 def check_select(host, args, n_sel, n_first=1, n_last=1):
