@@ -17,11 +17,28 @@
 
 namespace csa2 {
 
+namespace {
+// Per device: a kernel of this unit was launched, or captured, so its word may
+// be set; a device without one has nothing to copy (12 us of the call).
+std::atomic<bool> g_launched[256];
+
+void note_launch() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 256 &&
+      !g_launched[dev].load(std::memory_order_relaxed))
+    g_launched[dev].store(true, std::memory_order_release);
+}
+}  // namespace
+
 // Reads and clears this unit's device status word (the stream has been
 // synchronised).
 csa2_status kv8_take_status(uint32_t *v) {
   const uint32_t zero = 0;
   *v = 0;
+  int dev = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 256 &&
+      !g_launched[dev].load(std::memory_order_acquire))
+    return CSA2_OK;
   if (cudaMemcpyFromSymbol(v, g_device_status, sizeof(*v)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (*v && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero)) != cudaSuccess)
     return CSA2_ERR_CUDA;
@@ -337,6 +354,7 @@ csa2_status csa2_block_tables(const int32_t *lens, const int32_t *add, int32_t B
                            used, cap, B,     shift,      width,    n_free};
   const int64_t blocks = std::min<int64_t>(
       std::max<int64_t>({1, ceil_div(cap, kv8::kTableThreads), ceil_div(B, 64)}), device_sms());
+  note_launch();
   TraceScope ts("block_tables", as_stream(stream));
   kv8::block_tables_kernel<<<(unsigned)blocks, kv8::kTableThreads, (2 * size_t(B) + 1) * 4,
                              as_stream(stream)>>>(p);
@@ -367,6 +385,7 @@ csa2_status csa2_kv8_append(const csa2_kv8 *cache, const uint16_t *k_new, int64_
   // tokens: 32, so that fewer CTAs find no run (write and read back of 10,800
   // tokens of 4 heads 31.4 us, against 32.5 with 16)
   p.group = n <= 1024 ? 1 : kv8::kAppendGroup;
+  note_launch();
   TraceScope ts("kv8_append", as_stream(stream));
   return p.c.D == 64 ? launch_append_d<64>(p, as_stream(stream))
                      : launch_append_d<128>(p, as_stream(stream));
@@ -384,6 +403,7 @@ csa2_status csa2_kv8_unpack(const csa2_kv8 *cache, const int64_t *slots, int64_t
   const int64_t blocks = std::min<int64_t>(ceil_div(n * c.Hk * (c.D / 4), kv8::kUnpackThreads),
                                            int64_t(device_sms()) * 8);
   const dim3 grid((unsigned)blocks, 2);
+  note_launch();
   TraceScope ts("kv8_unpack", as_stream(stream));
   if (c.D == 64)
     kv8::kv8_unpack_kernel<64>
@@ -427,6 +447,7 @@ csa2_status csa2_kv8_select(const uint16_t *q, int64_t q_stride, const csa2_kv8 
   p.n_last = n_last;
   p.sel = sel;
   p.scores = static_cast<float *>(ws);
+  note_launch();
   return launch_select(p, as_stream(stream));
 }
 
@@ -468,6 +489,7 @@ csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *c
   p.sm_scale = sm_scale;
   p.out = out;
   p.lse = lse;
+  note_launch();
   const bool far = int64_t(B) * width * p.c.bs * p.c.Hk >= kBothReach;
   const AttnPlan plan = attn_plan(n, B, p.G, p.c.D, n_sel, far);
   return launch_attn(p, plan, static_cast<char *>(ws), as_stream(stream));

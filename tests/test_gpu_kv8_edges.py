@@ -1,5 +1,9 @@
 """Calls at the edge of what the 8-bit paged cache's documentation allows, on
 the GPU."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -79,6 +83,39 @@ def test_strides_that_address_nothing_are_not_looked_at():
     with pytest.raises(csa2.CSA2Error):
         csa2.kv8_attn(two, *args[1:])
     assert csa2.get_device_status() == 0
+
+
+# --- device status ------------------------------------------------------------
+
+STATUS = """
+import torch
+import compressed_sparse_attention_topk_b200 as csa2
+
+def copies():
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        code = csa2.get_device_status()
+        torch.cuda.synchronize()
+    return code, sum(1 for e in p.events() if "memcpy" in e.name.lower() and "dtoh" in e.name.lower())
+
+x = torch.tensor([-1], dtype=torch.int32, device="cuda")
+csa2.get_device_status()
+print(*copies())
+csa2.block_tables(x, x, x.view(1, 1).clone(), x.clone(), 16, 1)
+print(*copies())
+print(*copies())
+"""
+
+
+def test_status_is_one_copy_for_those_who_never_use_the_cache():
+    """And the cache's own word is read once it was used."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", STATUS], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = [tuple(map(int, x.split())) for x in r.stdout.split("\n") if x[:1].isdigit()]
+    if lines[-1][1] == 0:
+        pytest.skip("the profiler reports no copies here")
+    assert lines == [(0, 1), (4, 2), (0, 2)]
 
 
 # --- block tables -------------------------------------------------------------
