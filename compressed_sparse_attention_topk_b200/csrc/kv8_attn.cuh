@@ -138,14 +138,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // Beside the bytes it is the instructions around the products that bound it
 // (716 of a warp per unit of 8 KB at D = 128 and 8 rows, half of them the
 // codes' conversion): 32 decode tokens of 8 heads over 1.26 GB take 205 us
-// (6.1 TB/s) and the merge 8.  A tile of at most 4 rows therefore takes its logits in whole numbers: a query row is
-// scaled to 23 bits and split into three signed bytes, the columns of a
-// product hold the high and the middle bytes of row t side by side, a second
-// product the low ones, and 2^16 hi + 2^8 mid + lo is the exact dot of the
-// codes themselves, without their conversion (q is off by at most 2^-24 of
-// its row's largest magnitude).  A thread then has one row, so the softmax and
-// the outputs' arithmetic halve too: 576 instructions (lists of 32 blocks for
-// 1,024 tokens of 4 heads 305 -> 263 us).
+// (6.1 TB/s) and the merge 8.  A tile of at most 4 rows therefore takes its
+// logits in whole numbers: a query row is scaled to 30 bits and split into four
+// signed bytes d3 .. d0, the columns of a product hold d3 and d2 of row t side
+// by side, those of a second product d1 and d0, and 2^24 d3 + 2^16 d2 + 2^8 d1
+// + d0 is the dot with the codes themselves, without their conversion (q is off
+// by at most 2^-29 of its row's largest magnitude).  A thread then has one row,
+// so the softmax and the outputs' arithmetic halve too: 576 instructions (lists
+// of 32 blocks for 1,024 tokens of 4 heads 305 -> 268 us).
 // ---------------------------------------------------------------------------
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = 32 * kSplitWarps;
@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
     // ---- query rows.  Thread (g, t) holds dims 64 hh + 16 t + 4 w + 0 .. 3
     // for k-step 4 hh + w, as the cache's words below: of row g of each group
     // of 8, power-of-two scaled fp16 (0, 2 | 1, 3); or (QUAD) of row g / 2,
-    // bytes: high (g even) or middle (g odd), and low (g even) ----
+    // bytes: of the upper two the higher (g even) or the lower, and of the
+    // lower two ----
     uint32_t qb[R8][DT][2];
     float fac[R8][EC];     // of the thread's rows: the columns of S^T and O^T
     int row_pos[R8][EC];
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
       const float down = __uint_as_float(sb << 23);
       float f = p.sm_scale * 1.44269504088896340736f * __uint_as_float((254u - sb) << 23);
       if constexpr (QUAD) {
-        f *= 0x1p-21f;  // the digits stand for 2^22 times half the scaled value
+        f *= 0x1p-28f;  // the digits are of 2^28 times the scaled value
         // bytes carry no NaN or infinity: the row's scale does
         const uint32_t who = __ballot_sync(0xffffffffu, finite);
         if ((who >> (lane & 28) & 15u) != 15u) f = __int_as_float(0x7fffffff);
@@ -414,11 +415,12 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
           uint32_t upper = 0u, low = 0u;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int whole = __float2int_rn(y[e] * down * 0x1p21f);  // |.| <= 2^22
-            const int d0 = (int8_t)whole, rest = (whole - d0) >> 8;
-            const int d1 = (int8_t)rest, d2 = (rest - d1) >> 8;      // |d2| <= 64
-            upper |= (uint32_t)(uint8_t)(g & 1 ? d1 : d2) << (8 * e);
-            low |= (uint32_t)(uint8_t)(g & 1 ? 0 : d0) << (8 * e);
+            const int d0123 = __float2int_rn(y[e] * down * 0x1p28f);  // |.| <= 2^30
+            const int d0 = (int8_t)d0123, d123 = (d0123 - d0) >> 8;
+            const int d1 = (int8_t)d123, d23 = (d123 - d1) >> 8;
+            const int d2 = (int8_t)d23, d3 = (d23 - d2) >> 8;         // |d3| <= 64
+            upper |= (uint32_t)(uint8_t)(g & 1 ? d2 : d3) << (8 * e);
+            low |= (uint32_t)(uint8_t)(g & 1 ? d0 : d1) << (8 * e);
           }
           qb[q8][s][0] = upper;
           qb[q8][s][1] = low;
@@ -602,9 +604,9 @@ __global__ void __launch_bounds__(kSplitThreads, SplitShape<D, ROWS>::CTAS)
 #pragma unroll
               for (int e = 0; e < EC; ++e) {
                 float x;
-                if constexpr (QUAD)  // 2^16 hi + 2^8 mid < 2^29
-                  x = fmaf((float)(upper[2 * half] * 256 + upper[2 * half + 1]), 256.f,
-                           (float)low[2 * half]);
+                if constexpr (QUAD)  // 2^8 d3 + d2 < 2^29, 2^8 d1 + d0 < 2^30
+                  x = fmaf((float)(upper[2 * half] * 256 + upper[2 * half + 1]), 65536.f,
+                           (float)(low[2 * half] * 256 + low[2 * half + 1]));
                 else
                   x = dot[q8][half * 2 + e];
                 sc[q8][k][half * EC + e] = fmaf(x, fac[q8][e] * ks[k], -z[q8][e]);

@@ -240,3 +240,52 @@ def test_attn_a_missing_page_of_16_under_a_position_past_2_to_the_30(H, D, T):
     sel = torch.zeros((T, 2, 1), dtype=torch.int32, device="cuda")
     check_attn(*csa2.kv8_attn(*args, sel=sel), *want, info, T)
     assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("H,T", [(2, 1), (4, 2), (8, 1), (16, 1), (8, 40)])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 64)])
+def test_attn_queries_with_one_large_element(H, T, D, bs):
+    """A large element that meets zero codes: the logits are all the small ones'.
+
+    Beside the bounds of ref.attn_bounds a query element is held to 2^-29 of its
+    row's largest (sequences whose tiles have at most 4 rows) or 2^-25 (fp16,
+    the largest in [1, 2): the half step of an fp16 subnormal), so a logit may
+    be off by q_err max|q| sum_d |k_d| |sm_scale| more, and a weight and the sum
+    of weights by a factor of exp of that each."""
+    rng = np.random.default_rng(9)
+    Hk, lens, sm_scale = 2, [700, 90], 1e5
+    (q, c, table, cu, lens), _ = small_step(rng, lens, [T, 1], H, Hk, D, bs)
+    q = q * np.exp2(-rng.uniform(16, 22, q.shape))
+    q[:, :, 5] = 1.0
+    q = ref.bf16(q.astype(np.float32))
+    c["k"][..., 5] = 0
+    out, lse, info = ref.attn(q, c, table, cu, lens, None, sm_scale)
+    q_err = 2.0 ** -29 if T * H // Hk <= 4 else 2.0 ** -25
+    sums = np.abs(c["k"].astype(np.float64)).sum(-1).max(-1) * c["k_scale"]
+    logit = q_err * sums.max() * sm_scale
+    tol, tol_lse = ref.attn_bounds(out, lse, info)
+    tol = tol + np.expm1(2 * logit) * info[0]
+    got, got_lse = csa2.kv8_attn(dev_bf16(q), gpu_cache(c), dev(table), dev(cu), dev(lens),
+                                 sm_scale=sm_scale)
+    off = np.abs(got.float().cpu().numpy() - out) / tol
+    assert off.max() <= 1, off.max()
+    off = np.abs(got_lse.cpu().numpy() - lse) / (tol_lse + logit)
+    assert off.max() <= 1, off.max()
+    assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("H,T", [(4, 1), (8, 1), (4, 64)])
+def test_attn_queries_next_to_the_largest_number(H, T):
+    """Query elements of 2^127 and more, up to the largest bf16."""
+    rng = np.random.default_rng(10)
+    (q, c, table, cu, lens), _ = small_step(rng, [300], [T], H, 2, 128, 64)
+    big = ref.bf16(np.full(1, 3.3895313892515355e38, np.float32))[0]
+    q = ref.bf16(np.clip(q, -1, 1) * big)
+    q[..., ::7] = big
+    q[..., 1::7] = -big
+    sm_scale = 2.0 ** -126
+    out, lse, info = ref.attn(q, c, table, cu, lens, None, sm_scale)
+    got, got_lse = csa2.kv8_attn(dev_bf16(q), gpu_cache(c), dev(table), dev(cu), dev(lens),
+                                 sm_scale=sm_scale)
+    check_attn(got, got_lse, out, lse, info, T)
+    assert csa2.get_device_status() == 0
