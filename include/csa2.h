@@ -534,7 +534,8 @@ size_t csa2_kv8_select_workspace_size(int64_t n, int32_t Hk, int32_t width);
  * others up to n_sel in all, ties to the lower block.
  *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
  *   sel  device, int32 [n, Hk, n_sel] (output): blocks ascending, then -1
- *   ws   device workspace of ws_bytes >= csa2_kv8_select_workspace_size
+ *   ws   device workspace of ws_bytes >= csa2_kv8_select_workspace_size (n Hk
+ *        width scores), of one call at a time
  * A block whose page is outside the cache scores lowest of all.  Blocks past
  * the table's width are not there (recorded, bit 0): the last n_last are then
  * the table's last ones, not the token's own.
@@ -558,17 +559,29 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
  * listed blocks -- of values code * scale.  out = sum p * value rounded to
  * bf16 once, lse = natural log of sum exp(logit).  A token that sees nothing
  * (no position, an empty list, only skipped pages) gets out = 0, lse = -inf.
- * Where a sequence has more than 32 query rows (tokens times H / Hk) a value
- * scale below 2^-80 of the largest of its pages may count as 0.
  * A sequence with more new tokens than lens has tokens at negative positions,
  * which see nothing.
+ * Roundings: logits, maxima and sums are fp32 (lse is of unrounded weights).
+ * Before they meet the values, softmax weights (in the kernel for many rows
+ * weights times value scale) are rounded once to fp16: off by 2^-11 of
+ * themselves or 2^-35 of the row's largest, whichever is more.  A query element is held to 2^-25 of its row's largest (fp16 of the row times
+ * a power of two), or 2^-29 (tiles of at most 4 rows).  Logits beyond 2^100
+ * and value scales outside 2^-75 .. 2^75, other than 0, may overflow or lose
+ * bits.  Query rows of a sequence: its tokens times H / Hk.  Where any
+ * sequence of the call has more than 32, or n H / Hk > 32 B, the kernel for
+ * many rows may serve the others too, and a value scale below 2^-80 of the
+ * largest of its sequence's pages may count as 0.
+ * Padding counts: which kernel serves a call goes by n, B and width, as the
+ * host knows them, not by cu[B] or lens.  A step padded to many more tokens
+ * than it has is right, but may run on the kernel for many rows.
  *   q    device, bf16 [n, H, D], stride in elements (16-byte aligned)
  *   sel  device, int32 [n, Hk, n_sel] with n_sel >= 1, or NULL and n_sel 0
  *        (every block): block numbers of the sequence, each at most once, a
  *        negative one is skipped
  *   out  device, bf16 [n, H, D] (16-byte aligned); lse device, fp32 [n, H] or
  *        NULL
- *   ws   device workspace of ws_bytes >= csa2_kv8_attn_workspace_size
+ *   ws   device workspace of ws_bytes >= csa2_kv8_attn_workspace_size, of one
+ *        call at a time (two captured graphs that may run at once need two)
  * Supported: H a multiple of Hk, H <= 128, n * H < 2^31, n_sel <= 65536,
  * B <= 4096, width * block <= 2^30, sm_scale finite. */
 csa2_status csa2_kv8_attn(const uint16_t *q, int64_t q_stride, const csa2_kv8 *cache,

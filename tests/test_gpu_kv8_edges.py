@@ -289,3 +289,36 @@ def test_attn_queries_next_to_the_largest_number(H, T):
                                  sm_scale=sm_scale)
     check_attn(got, got_lse, out, lse, info, T)
     assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 5, 200])
+@pytest.mark.parametrize("scale", [2.0 ** -75, 2.0 ** 75])
+def test_attn_value_scales_at_the_ends_of_their_range(T, scale):
+    """Pages of the smallest or the largest value scale, flat weights over
+    thousands of positions: nothing overflows or loses bits."""
+    rng = np.random.default_rng(11)
+    (q, c, table, cu, lens), args = small_step(rng, [5000, 300], [T, 1], 8, 2, 64, 64)
+    c["v_scale"][:] = np.float32(scale)
+    c["v"][:] = np.where(c["v"] >= 20, 127, c["v"])
+    out, lse, info = ref.attn(q, c, table, cu, lens, None, 0.01)
+    got, got_lse = csa2.kv8_attn(args[0], gpu_cache(c), *args[2:], sm_scale=0.01)
+    # (the bounds' absolute 1e-30 is 1e-8 of the smallest scale)
+    check_attn(got, got_lse, out, lse, info, len(q))
+    assert np.abs(out).max() > 8 * scale
+    assert csa2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("G,rows", [(1, 33), (4, 9)])
+def test_attn_value_scales_far_apart_beside_a_long_sequence(G, rows):
+    """What the header says of one token beside a sequence of more than 32 query
+    rows: scales down to 2^-80 of the largest count."""
+    rng = np.random.default_rng(12)
+    (q, c, table, cu, lens), args = small_step(rng, [200, 150], [2 * rows, 1], 2 * G, 2, 64, 16)
+    c["v_scale"][:] = 1.0
+    c["v_scale"][table[1, 1:4]] = np.float32(2.0 ** -79)
+    c["k"][table[1, 1]] = 127          # a page that takes nearly all the weight
+    q[-1] = 0.5
+    out, lse, info = ref.attn(q, c, table, cu, lens, None, 1.0)
+    got, got_lse = csa2.kv8_attn(dev_bf16(q), gpu_cache(c), *args[2:], sm_scale=1.0)
+    check_attn(got, got_lse, out, lse, info, len(q))
+    assert csa2.get_device_status() == 0
