@@ -600,7 +600,8 @@ def block_tables(lens, add, table, free_pages, block: int, cap: int, out=None):
 class KV8Cache:
     """The tensors of an 8-bit paged cache, checked and marshalled once: int8
     k, v [pages, Hk, block, D], fp32 k_scale, v_scale [pages, Hk], int16 k_sum
-    [pages, Hk, D] (contiguous CUDA tensors, kept alive by this handle)."""
+    [pages, Hk, D] (contiguous CUDA tensors, kept alive by this handle, which
+    takes no others later)."""
 
     def __init__(self, k, v, k_scale, v_scale, k_sum):
         torch = _kv8_types()[0]
@@ -622,6 +623,13 @@ class KV8Cache:
         self._c = KV8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_sum), P, Hk,
                       self.block, D)
         self._ref = ctypes.byref(self._c)
+
+    def __setattr__(self, name, value):
+        # the calls go by the pointers marshalled above: another tensor in an
+        # attribute would leave them at memory that nothing keeps
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{name}: the tensors of a KV8Cache stay, make a new one")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def empty(cls, pages: int, Hk: int, block: int, D: int, device="cuda") -> "KV8Cache":

@@ -118,6 +118,18 @@ def test_status_is_one_copy_for_those_who_never_use_the_cache():
     assert lines == [(0, 1), (4, 2), (0, 2)]
 
 
+# --- the handle ---------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "k_sum", "pages", "D"])
+def test_a_cache_keeps_the_tensors_that_it_was_made_of(name):
+    """Its calls go by their pointers."""
+    c = csa2.KV8Cache.empty(3, 2, 16, 64)
+    old = getattr(c, name)
+    with pytest.raises(AttributeError):
+        setattr(c, name, old.clone() if torch.is_tensor(old) else old + 1)
+    assert getattr(c, name) is old
+
+
 # --- block tables -------------------------------------------------------------
 
 @pytest.mark.parametrize("B,cap", [(3, 9), (0, 2), (2, 0)])
