@@ -605,31 +605,28 @@ class KV8Cache:
 
     def __init__(self, k, v, k_scale, v_scale, k_sum):
         torch = _kv8_types()[0]
-        self.k, self.v = _dev(k, "k", torch.int8), _dev(v, "v", torch.int8)
-        self.k_scale = _dev(k_scale, "k_scale", torch.float32)
-        self.v_scale = _dev(v_scale, "v_scale", torch.float32)
-        self.k_sum = _dev(k_sum, "k_sum", torch.int16)
+        k, v = _dev(k, "k", torch.int8), _dev(v, "v", torch.int8)
+        k_scale = _dev(k_scale, "k_scale", torch.float32)
+        v_scale = _dev(v_scale, "v_scale", torch.float32)
+        k_sum = _dev(k_sum, "k_sum", torch.int16)
         if k.dim() != 4:
             raise ValueError("k must be [pages, Hk, block, D]")
-        self.pages, self.Hk, self.block, self.D = k.shape
-        P, Hk, D = self.pages, self.Hk, self.D
+        P, Hk, block, D = k.shape
         if (v.shape != k.shape or k_scale.shape != (P, Hk) or v_scale.shape != (P, Hk)
                 or k_sum.shape != (P, Hk, D)):
             raise ValueError("v must be like k, k_scale and v_scale [pages, Hk], k_sum "
                              "[pages, Hk, D]")
-        self.device = k.get_device()
-        if any(x.get_device() != self.device for x in (v, k_scale, v_scale, k_sum)):
+        device = k.get_device()
+        if any(x.get_device() != device for x in (v, k_scale, v_scale, k_sum)):
             raise ValueError("the tensors of a cache must be on one device")
-        self._c = KV8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_sum), P, Hk,
-                      self.block, D)
-        self._ref = ctypes.byref(self._c)
+        c = KV8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(k_sum), P, Hk, block, D)
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, k_sum=k_sum, pages=P,
+                             Hk=Hk, block=block, D=D, device=device, _c=c, _ref=ctypes.byref(c))
 
     def __setattr__(self, name, value):
         # the calls go by the pointers marshalled above: another tensor in an
         # attribute would leave them at memory that nothing keeps
-        if "_ref" in self.__dict__:
-            raise AttributeError(f"{name}: the tensors of a KV8Cache stay, make a new one")
-        object.__setattr__(self, name, value)
+        raise AttributeError(f"{name}: the tensors of a KV8Cache stay, make a new one")
 
     @classmethod
     def empty(cls, pages: int, Hk: int, block: int, D: int, device="cuda") -> "KV8Cache":

@@ -145,7 +145,10 @@ void launch_score(const kv8::SelectParams &p, dim3 grid, cudaStream_t st) {
 constexpr int32_t kPickStaged = 40960;
 
 csa2_status launch_select(const kv8::SelectParams &p, cudaStream_t st) {
-  // tiles of 32 tokens where sequences have that many on average; the blocks
+  // tiles of 32 tokens where sequences have that many on average, else of 8
+  // (both kernels, D = 128: 4 sequences of 4 tokens and 262,144 positions 27 us
+  // with 8, 31 with 32; of 24 to 64 tokens and 65,536 positions the same within
+  // 2 us; 64 sequences of 40 tokens and 8,192 positions 39 and 37); the blocks
   // split so that about three CTAs per SM share the work (each forms its
   // tokens' queries anew: a 4,096-token chunk 76 us with one split, 84 with two)
   const int32_t TT = p.s.n >= int64_t(32) * p.s.B ? 32 : 8;
@@ -164,6 +167,9 @@ csa2_status launch_select(const kv8::SelectParams &p, cudaStream_t st) {
   }
   const int64_t rows = p.s.n * p.c.Hk;
   TraceScope ts("kv8_pick", st);
+  // a warp per row up to 2,048 blocks: as fast as a CTA per row for a few rows
+  // (both kernels, 4 tokens: 14-21 us and 14-19), twice as fast for many (1,024
+  // tokens over 2,048 blocks 50 us, 94 with a CTA per row)
   const dim3 warps((unsigned)ceil_div(rows, kv8::kPickWarps));
   if (p.s.width <= 256)
     return launch_dependent(kv8::kv8_pick_warp_kernel<8>, warps, 32 * kv8::kPickWarps, 0, st, p);
@@ -199,13 +205,22 @@ struct AttnPlan {
 // Sequences of up to 32 query rows (tokens x heads of a group) belong to the
 // split stream, with as many rows in a tile as they have -- every row of a
 // tile reads the same fragments of the cache -- and longer ones to the
-// tensor-core tiles.  The host knows the numbers of tokens and sequences only.
+// tensor-core tiles.  Both kernels on both sides (us, split stream / tcgen05
+// tiles, 2 kv heads, D = 128): 4 sequences of 65,536 positions with 24 rows
+// 64 / 152, 32 rows 88 / 156, 40 rows (two tiles) 139 / 156, 64 rows 139 / 158,
+// 96 rows 199 / 160, 256 rows 461 / 178; 16 sequences of 4,096 positions and 4
+// kv heads with 32 rows 66 / 78, 40 rows 90 / 78, 64 rows 92 / 80.  The exception
+// is a long context alone: one sequence of 262,144 positions with 40 to 64 rows
+// takes 240 us here, 135 as two tiles of the split stream.
+// The host knows the numbers of tokens and sequences only.
 // Where one of several sequences may have a tile's 256 rows beyond a token for
 // each, both kernels run, each on its own sequences (31 decode tokens of
 // 32,768 positions and 512 tokens of 16,384 in one step: 320 us instead of 760;
 // a kernel that finds no sequence costs about 8 us, so not where the tables
 // reach fewer than 2^17 positions and kv heads in all: what one kernel loses
-// there is of that size); else the average decides.
+// there is of that size; tables far wider than their sequences lose nothing, 7
+// decode tokens of 500 positions and a prompt of 300 55 us with either plan, of
+// 2,000 64 us with both kernels and 72 with one); else the average decides.
 // The split stream's tile is then the average, or a decode token's group where
 // the tokens cannot be the same for all.  With lists everything is the split
 // stream's, by the heads of a group.
@@ -382,8 +397,11 @@ csa2_status csa2_kv8_append(const csa2_kv8 *cache, const uint16_t *k_new, int64_
   p.slots = slots;
   p.n = n;
   // a decode step: a token per CTA, so that its runs go side by side; more
-  // tokens: 32, so that fewer CTAs find no run (write and read back of 10,800
-  // tokens of 4 heads 31.4 us, against 32.5 with 16)
+  // tokens: 32, so that fewer CTAs find no run.  The host does not know which
+  // it is (us for a run per token / one prompt, 4 heads): 512 tokens 27 / 14
+  // with 1, 84 / 12 with 32; 1,024: 41 / 16 and 86 / 12; 2,048: 74 / 23 and 98 /
+  // 14; 4,096: 137 / 35 and 133 / 16.  (10,800 tokens written and read back: 31.4
+  // us, 32.5 with 16.)
   p.group = n <= 1024 ? 1 : kv8::kAppendGroup;
   note_launch();
   TraceScope ts("kv8_append", as_stream(stream));

@@ -5,10 +5,10 @@
 //   x_j = (sm_scale log2(e) ks) <q, kcode_j>,  p_j = 2^(x_j - m),
 //   out = sum_j p_j vs vcode_j / sum_j p_j,   lse = ln 2 (m + log2 sum_j p_j)
 // in one pass over the keys with the running maximum m.  The codes are exact
-// in fp16, and so is q once its row is scaled by a power of two (its largest
-// magnitude goes to [1, 2); what is more than 2^-14 below it loses bits that
-// weigh less than fp32's in the dot), so the products are exact and their
-// sums fp32.  m follows the running maximum only when that has grown by more
+// in fp16, and so is q once its row is scaled by a power of two: its largest
+// magnitude goes to [1, 2), and an element less than 2^-17 of that is off by at
+// most 2^-25 of it (half the last place of an fp16 subnormal).  So the products
+// are exact and their sums fp32.  m follows the running maximum only when that has grown by more
 // than kSlack, which one vote of the warp finds out; so a row's maximum is
 // seldom reduced and its output seldom rescaled.  The weights are rounded once
 // to fp16, 2^10 at m: 2^-11 of each weight, and weights down to 2^-34 of the
@@ -136,7 +136,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // be mostly padding.
 //
 // Beside the bytes it is the instructions around the products that bound it
-// (716 of a warp per unit of 8 KB at D = 128 and 8 rows, half of them the
+// (717 of a warp per unit of 8 KB at D = 128 and 8 rows, half of them the
 // codes' conversion): 32 decode tokens of 8 heads over 1.26 GB take 205 us
 // (6.1 TB/s) and the merge 8.  A tile of at most 4 rows therefore takes its
 // logits in whole numbers: a query row is scaled to 30 bits and split into four
@@ -144,7 +144,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // by side, those of a second product d1 and d0, and 2^24 d3 + 2^16 d2 + 2^8 d1
 // + d0 is the dot with the codes themselves, without their conversion (q is off
 // by at most 2^-29 of its row's largest magnitude).  A thread then has one row,
-// so the softmax and the outputs' arithmetic halve too: 576 instructions (lists
+// so the softmax and the outputs' arithmetic halve too: 585 instructions (lists
 // of 32 blocks for 1,024 tokens of 4 heads 305 -> 268 us).
 // ---------------------------------------------------------------------------
 constexpr int kSplitWarps = 4;

@@ -12,9 +12,11 @@
 // for a chunk.  kv8_pick_*_kernel then takes each row's n_sel best: a score is
 // ordered as an unsigned key, forced blocks get the largest key, and the
 // n_sel-th largest key is found by bisection within a warp (rows of up to
-// 2,048 blocks) or by digits over a CTA.  One token over 4,096 blocks is bound
-// by latency (10 and 9 us); 4,096 tokens over 1,024 blocks and 4 heads by
-// instructions (50 and 40 us).
+// 2,048 blocks) or by digits over a CTA.  Four tokens over 4,096 blocks are
+// bound by latency (11 and 11 us, 17 MB).  4,096 tokens over 1,024 blocks and 4
+// heads move 67 MB of scores to L2 and back beside 18 MB of sums (42 and 42 us;
+// instructions issue in 43 and 72 % of the cycles): that traffic is this cut's,
+// not the operator's, whose own bytes take 3 us.
 #pragma once
 
 #include "kv8_cache.cuh"
