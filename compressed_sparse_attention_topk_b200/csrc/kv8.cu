@@ -18,15 +18,13 @@
 namespace csa2 {
 
 namespace {
-// Per device: a kernel of this unit was launched, or captured, so its word may
-// be set; a device without one has nothing to copy (12 us of the call).
-std::atomic<bool> g_launched[256];
+// A kernel of this unit was launched, or captured, so its word may be set: a
+// process that never uses the cache has nothing to copy (12 us of the call).
+std::atomic<bool> g_launched{false};
 
 void note_launch() {
-  int dev = -1;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 256 &&
-      !g_launched[dev].load(std::memory_order_relaxed))
-    g_launched[dev].store(true, std::memory_order_release);
+  if (!g_launched.load(std::memory_order_relaxed))
+    g_launched.store(true, std::memory_order_release);
 }
 }  // namespace
 
@@ -35,10 +33,7 @@ void note_launch() {
 csa2_status kv8_take_status(uint32_t *v) {
   const uint32_t zero = 0;
   *v = 0;
-  int dev = -1;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 256 &&
-      !g_launched[dev].load(std::memory_order_acquire))
-    return CSA2_OK;
+  if (!g_launched.load(std::memory_order_acquire)) return CSA2_OK;
   if (cudaMemcpyFromSymbol(v, g_device_status, sizeof(*v)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (*v && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero)) != cudaSuccess)
     return CSA2_ERR_CUDA;
