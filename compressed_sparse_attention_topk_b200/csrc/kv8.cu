@@ -395,7 +395,7 @@ csa2_status csa2_kv8_append(const csa2_kv8 *cache, const uint16_t *k_new, int64_
   // tokens: 32, so that fewer CTAs find no run.  The host does not know which
   // it is (us for a run per token / one prompt, 4 heads): 512 tokens 27 / 14
   // with 1, 84 / 12 with 32; 1,024: 41 / 16 and 86 / 12; 2,048: 74 / 23 and 98 /
-  // 14; 4,096: 137 / 35 and 133 / 16.  (10,800 tokens written and read back: 31.4
+  // 14; 4,096: 137 / 35 and 133 / 16.  (10,241 tokens written and read back: 31.4
   // us, 32.5 with 16.)
   p.group = n <= 1024 ? 1 : kv8::kAppendGroup;
   note_launch();

@@ -137,7 +137,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 //
 // Beside the bytes it is the instructions around the products that bound it
 // (717 of a warp per unit of 8 KB at D = 128 and 8 rows, half of them the
-// codes' conversion): 32 decode tokens of 8 heads over 1.26 GB take 205 us
+// codes' conversion): 28 decode tokens of 8 heads over 1.26 GB take 205 us
 // (6.1 TB/s) and the merge 8.  A tile of at most 4 rows therefore takes its
 // logits in whole numbers: a query row is scaled to 30 bits and split into four
 // signed bytes d3 .. d0, the columns of a product hold d3 and d2 of row t side

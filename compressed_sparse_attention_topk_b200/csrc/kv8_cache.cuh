@@ -24,7 +24,7 @@ struct Cache {
 // gather per token and a copy per new page.  Latency-bound: B <= 4096 lengths
 // are 32 KB, so every CTA repeats the scan (L2 reads) instead of waiting for
 // another one's, and the tokens are dealt over the CTAs (6 us for 32 requests
-// of a token as for 512 of 59,000).
+// of a token as for 512 of 69,792).
 // ---------------------------------------------------------------------------
 constexpr int kTableThreads = 512;
 
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 // scale, requantised old codes if the scale grew, new codes, and for keys the
 // code sums.  Bound by bytes (4 D read + 2 D written per token and head; a
 // decode step's page is mostly its earlier rows), in practice by the chain
-// slots -> rows -> scale -> codes of a run: 6.5 us for 32 tokens of 4 heads,
-// 17 us for 10,800 (33 MB, 1.9 TB/s; instructions issue in 53 % of the cycles,
+// slots -> rows -> scale -> codes of a run: 6.5 us for 28 tokens of 4 heads,
+// 18 us for 10,241 (31 MB, 1.7 TB/s; instructions issue in 53 % of the cycles,
 // and between them a warp waits for rows, code and barriers in equal parts).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Append
 // ---------------------------------------------------------------------------
 // The reader: one thread per 4 codes of a row and head, so that a warp reads
 // 128 bytes and writes 512 in one piece.  Bound by bytes (D read and 4 D
-// written per row, head and array): 11,500 rows of 4 heads (59 MB) in 15 us (issue 64 %, else waiting for the codes).
+// written per row, head and array): 10,496 rows of 4 heads (54 MB) in 16 us
+// (instructions issue in 64 % of the cycles, else the warps wait for the codes).
 // ---------------------------------------------------------------------------
 constexpr int kUnpackThreads = 256;
 
