@@ -210,7 +210,7 @@ struct AttnPlan {
 // The host knows the numbers of tokens and sequences only.
 // Where one of several sequences may have a tile's 256 rows beyond a token for
 // each, both kernels run, each on its own sequences (31 decode tokens of
-// 32,768 positions and 512 tokens of 16,384 in one step: 320 us instead of 760;
+// 32,768 positions and 512 tokens of 16,384 in one step: 320 us instead of 768;
 // a kernel that finds no sequence costs about 8 us, so not where the tables
 // reach fewer than 2^17 positions and kv heads in all: what one kernel loses
 // there is of that size; tables far wider than their sequences lose nothing, 7
