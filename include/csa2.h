@@ -566,8 +566,9 @@ size_t csa2_kv8_attn_workspace_size(int64_t n, int32_t B, int32_t H, int32_t Hk,
  * weights times value scale) are rounded once to fp16: off by 2^-11 of
  * themselves or 2^-35 of the row's largest, whichever is more.  A query
  * element is held to 2^-25 of its row's largest (fp16 of the row times a
- * power of two), or 2^-29 (tiles of at most 4 rows).  Logits beyond 2^100 and
- * value scales outside 2^-75 .. 2^75, other than 0, may overflow or lose bits.
+ * power of two), or 2^-29 (tiles of at most 4 rows).  Logits beyond 2^100,
+ * and other than 0 an |sm_scale| outside 2^-126 .. 2^100 or value scales outside
+ * 2^-75 .. 2^75, may overflow or lose bits.
  * Query rows of a sequence: its tokens times H / Hk.  Where any sequence of
  * the call has more than 32, or n H / Hk > 32 B, the kernel for many rows may
  * serve the others too, and a value scale below 2^-80 of the largest of its
