@@ -37,8 +37,8 @@ def test_lists_of_no_token(lib, kw, rc):
     assert attn(lib, **kw) == rc
 
 
-# places of 1 KiB apart: B = 3, width 4, 5 free pages, cap 8
-PLACES = dict(lens=(1024, 12), add=(2048, 12), table=(3072, 48), free=(4096, 20),
+# places 1 KiB apart or more: B = 3, width 4, 5 free pages, cap 8
+PLACES = dict(lens=(1024, 12), add=(2048, 12), table=(10240, 48), free=(4096, 20),
               lens_out=(5120, 12), cu=(6144, 16), slots=(7168, 64), pos=(8192, 32),
               used=(9216, 4))
 WRITTEN = ("table", "lens_out", "cu", "slots", "pos", "used")
